@@ -1,5 +1,6 @@
-"""moeq: NF4 / row-wise int8 quantization of fused MoE expert tensors and the
-routed experts forward straight from the packed storage, on MI355X (gfx950).
+"""moeq: NF4 / row-wise int8 / MXFP4 quantization of fused MoE expert tensors,
+the routed experts forward straight from the packed storage, products grouped
+by expert with their gradients, and gradient clipping, on MI355X (gfx950).
 
 This module is a thin ctypes binding over ``libmoeq.so`` (declared in
 ``include/moeq.h``): it marshals torch tensors into device pointers and the
@@ -9,6 +10,8 @@ there is no fallback.  A missing library is an error, never a silent switch
 to another path.
 """
 
+import array
+import contextlib
 import ctypes
 import os
 
@@ -25,12 +28,17 @@ __all__ = [
     "moeq_qweight_copy_async", "FMT_NF4_DQ", "DQ_GROUP", "moeq_compress_absmax",
     "moeq_stream_reference", "moeq_router_route", "moeq_experts_forward_routed", "Routing",
     "moeq_experts_forward_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "FMT_MXFP4", "MXFP4_BLOCKSIZE", "moeq_quantize_mxfp4", "moeq_grouped_mm", "moeq_grouped_mm_grad_input",
+    "moeq_grouped_mm_grad_weight", "moeq_grouped_mm_mxfp4", "moeq_clip_grad_norm_workspace_bytes",
+    "moeq_clip_grad_norm",
 ]
 
 FMT_NF4 = 1
 FMT_INT8_ROWWISE = 2
 FMT_NF4_DQ = 3
+FMT_MXFP4 = 4
 NF4_BLOCKSIZE = 64
+MXFP4_BLOCKSIZE = 32
 DQ_GROUP = 256
 ABI_VERSION = 3
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -92,6 +100,14 @@ def _load():
         "moeq_experts_forward_save": (I32, [P, P, P, I32, I32, QP, QP, P, P, P, SZ, P]),
         "moeq_experts_backward_saved_workspace_bytes": (SZ, [I32, I32, QP, QP]),
         "moeq_experts_backward_saved": (I32, [P, P, I32, I32, QP, QP, P, P, P, P, P, SZ, P]),
+        "moeq_quantize_mxfp4": (I32, [P, QP, P]),
+        "moeq_dequantize_mxfp4": (I32, [QP, P, P]),
+        "moeq_grouped_mm": (I32, [P, P, P, I32, I32, I32, I32, P, P]),
+        "moeq_grouped_mm_grad_input": (I32, [P, P, P, I32, I32, I32, I32, P, P]),
+        "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P]),
+        "moeq_grouped_mm_mxfp4": (I32, [QP, QP, P, P, P]),
+        "moeq_clip_grad_norm_workspace_bytes": (SZ, [I32]),
+        "moeq_clip_grad_norm": (I32, [P, I32, ctypes.c_double, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -164,6 +180,20 @@ def _on_device(where, *tensors):
     return dev
 
 
+def _current(dev):
+    """Context in which ``dev`` is the current device (a launch goes to a
+    stream of the current device)."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _used_on(stream, *tensors):
+    """Tensors made here (on the current stream) that a call on ``stream`` uses
+    keep their memory until that work is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _match_qweight(q, shape, formats, name):
     """q is a QWeight of one of ``formats`` describing ``shape`` [E, rows, cols]."""
     if not isinstance(q, QWeight):
@@ -221,14 +251,17 @@ class QWeight:
     ``[E, rows*cols/64]``.  int8: ``qdata`` int8 ``[E, rows, cols]``,
     ``scales`` fp32 ``[E, rows]``.  NF4 with double-quantized absmax: NF4
     ``qdata``, ``scale_codes`` uint8 ``[E, rows*cols/64]`` and ``scales``
-    fp32 group scales ``[E, ceil(rows*cols/64 / 256)]``.  Plain tensors, so
-    they serialise with ``torch.save``.
+    fp32 group scales ``[E, ceil(rows*cols/64 / 256)]``.  MXFP4: ``qdata``
+    uint8 ``[E, rows, cols/2]`` (the even column in the low nibble),
+    ``scale_codes`` uint8 ``[E, rows, cols/32]`` and no ``scales``.  Plain
+    tensors, so they serialise with ``torch.save``.
     """
 
     def __init__(self, fmt, num_experts, rows, cols, qdata, scales, scale_codes=None):
         self.format = fmt
         self.num_experts, self.rows, self.cols = int(num_experts), int(rows), int(cols)
-        self.blocksize = NF4_BLOCKSIZE if fmt in (FMT_NF4, FMT_NF4_DQ) else self.cols
+        self.blocksize = {FMT_NF4: NF4_BLOCKSIZE, FMT_NF4_DQ: NF4_BLOCKSIZE,
+                          FMT_MXFP4: MXFP4_BLOCKSIZE}.get(fmt, self.cols)
         self.qdata, self.scales, self.scale_codes = qdata, scales, scale_codes
 
     @classmethod
@@ -246,6 +279,10 @@ class QWeight:
         elif fmt == FMT_INT8_ROWWISE:
             q = torch.empty((E, R, C), dtype=torch.int8, device=device)
             s = torch.empty((E, R), dtype=torch.float32, device=device)
+        elif fmt == FMT_MXFP4:
+            q = torch.empty((E, R, C // 2), dtype=torch.uint8, device=device)
+            s = None
+            codes = torch.empty((E, R, C // MXFP4_BLOCKSIZE), dtype=torch.uint8, device=device)
         else:
             raise ValueError(f"unknown format {fmt}")
         return cls(fmt, E, R, C, q, s, codes)
@@ -263,14 +300,15 @@ class QWeight:
     def expert(self, e):
         """Expert ``e`` alone (E = 1), sharing storage."""
         codes = self.scale_codes[e:e + 1] if self.scale_codes is not None else None
-        return QWeight(self.format, 1, self.rows, self.cols, self.qdata[e:e + 1], self.scales[e:e + 1], codes)
+        scales = self.scales[e:e + 1] if self.scales is not None else None
+        return QWeight(self.format, 1, self.rows, self.cols, self.qdata[e:e + 1], scales, codes)
 
     def like(self, device, pin_memory=False):
         """An empty QWeight of the same format and shape on ``device`` (host
         tensors pinned when ``pin_memory``)."""
-        new = [torch.empty(t.shape, dtype=t.dtype, device=device, pin_memory=pin_memory) for t in self._tensors()]
-        codes = new[2] if len(new) == 3 else None
-        return QWeight(self.format, self.num_experts, self.rows, self.cols, new[0], new[1], codes)
+        new = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device, pin_memory=pin_memory)
+               for t in (self.qdata, self.scales, self.scale_codes)]
+        return QWeight(self.format, self.num_experts, self.rows, self.cols, *new)
 
     def layout(self):
         """``[(name, shape, dtype)]`` of the tensors this format and shape need."""
@@ -284,6 +322,8 @@ class QWeight:
                           ("scale_codes", (E, nb), torch.uint8)]
         if self.format == FMT_INT8_ROWWISE:
             return [("qdata", (E, R, C), torch.int8), ("scales", (E, R), torch.float32)]
+        if self.format == FMT_MXFP4:
+            return [("qdata", (E, R, C // 2), torch.uint8), ("scale_codes", (E, R, C // MXFP4_BLOCKSIZE), torch.uint8)]
         raise ValueError(f"unknown format {self.format}")
 
     def validate_layout(self):
@@ -291,9 +331,13 @@ class QWeight:
         shape need and is contiguous.  Raises ValueError / TypeError."""
         if self.format in (FMT_NF4, FMT_NF4_DQ) and self.cols % NF4_BLOCKSIZE != 0:
             raise ValueError(f"NF4 needs cols % {NF4_BLOCKSIZE} == 0, got cols={self.cols}")
+        if self.format == FMT_MXFP4 and self.cols % MXFP4_BLOCKSIZE != 0:
+            raise ValueError(f"MXFP4 needs cols % {MXFP4_BLOCKSIZE} == 0, got cols={self.cols}")
         lay = self.layout()
-        if self.format != FMT_NF4_DQ and self.scale_codes is not None:
-            raise ValueError("scale_codes is only used by the double-quantized NF4 format")
+        if self.format not in (FMT_NF4_DQ, FMT_MXFP4) and self.scale_codes is not None:
+            raise ValueError("scale_codes is only used by the double-quantized NF4 and the MXFP4 format")
+        if self.format == FMT_MXFP4 and self.scales is not None:
+            raise ValueError("scales is not used by the MXFP4 format")
         for name, shape, dtype in lay:
             t = getattr(self, name)
             if not isinstance(t, torch.Tensor):
@@ -326,9 +370,8 @@ class QWeight:
 
     def _desc(self):
         """The C descriptor, for a caller that has validated this QWeight."""
-        codes = self.scale_codes.data_ptr() if self.scale_codes is not None else None
         return _QW(self.format, self.num_experts, self.rows, self.cols, self.blocksize,
-                   self.qdata.data_ptr(), self.scales.data_ptr(), codes)
+                   self.qdata.data_ptr(), _ptr(self.scales), _ptr(self.scale_codes))
 
 
 def moeq_abi_version():
@@ -415,6 +458,30 @@ def moeq_quantize_int8_rowwise(w, out=None, stream=None):
     return q
 
 
+def moeq_quantize_mxfp4(w, out=None, stream=None):
+    """bf16 ``[E, rows, cols]`` (weights) or ``[rows, cols]`` (activations;
+    E = 1) -> MXFP4 :class:`QWeight`: blocks of 32 columns with one
+    power-of-two scale.  A block with an infinity or a NaN becomes NaN."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a [E, rows, cols] or [rows, cols] tensor")
+    _dev(w, torch.bfloat16, "w")
+    shape = tuple(w.shape) if w.dim() == 3 else (1, *w.shape)
+    if shape[2] % MXFP4_BLOCKSIZE != 0:
+        raise ValueError(f"MXFP4 needs cols % {MXFP4_BLOCKSIZE} == 0, got cols={shape[2]}")
+    if out is not None:
+        _match_qweight(out, shape, (FMT_MXFP4,), "out")
+        out.validate_layout()
+    dev = _on_device("moeq_quantize_mxfp4", w, *(out._tensors() if out is not None else []))
+    q = out if out is not None else QWeight.empty(FMT_MXFP4, *shape, device=dev)
+    if w.numel():
+        qc = q._desc()
+        with _current(dev):
+            _check(_load().moeq_quantize_mxfp4(_ptr(w), ctypes.byref(qc), _stream(stream, dev)), "moeq_quantize_mxfp4")
+    if out is None:
+        _used_on(stream, *q._tensors())
+    return q
+
+
 def moeq_dequantize(q, out=None, stream=None):
     """:class:`QWeight` -> bf16 ``[E, rows, cols]``."""
     if not isinstance(q, QWeight):
@@ -422,7 +489,18 @@ def moeq_dequantize(q, out=None, stream=None):
     q.validate_layout()
     if out is not None:
         _dev(out, torch.bfloat16, "out", q.shape)
-    _on_device("moeq_dequantize", *q._tensors(), out)
+    dev = _on_device("moeq_dequantize", *q._tensors(), out)
+    if q.format == FMT_MXFP4:
+        made = out is None
+        if made:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        qc = q._desc()
+        with _current(dev):
+            _check(_load().moeq_dequantize_mxfp4(ctypes.byref(qc), _ptr(out), _stream(stream, dev)),
+                   "moeq_dequantize_mxfp4")
+        if made:
+            _used_on(stream, out)
+        return out
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.qdata.device)
     qc = q._c()
@@ -742,3 +820,165 @@ def moeq_route_buckets(top_k_index, num_experts, workspace=None, stream=None):
                                   _ptr(perm), _ptr(slot), _ptr(workspace), workspace.numel(),
                                   _stream(stream)), "moeq_route_buckets")
     return counts, offsets, perm, slot
+
+
+def _grouped_rows(rows, w, offsets, names):
+    """(M, E, N, K) of rows [M, N or K] bf16 and w [E, N, K] bf16 with
+    offsets [E+1] int32, structurally checked.  names: of rows, and whether
+    its columns are N or K."""
+    name, cols = names
+    if not isinstance(rows, torch.Tensor) or rows.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be a [E, N, K] tensor")
+    _dev(rows, torch.bfloat16, name)
+    _dev(w, torch.bfloat16, "w")
+    E, N, K = w.shape
+    want = N if cols == "N" else K
+    if rows.shape[1] != want:
+        raise ValueError(f"{name} must have {want} columns (w is {tuple(w.shape)}), got {rows.shape[1]}")
+    _dev(offsets, torch.int32, "offsets", (E + 1,))
+    return int(rows.shape[0]), int(E), int(N), int(K)
+
+
+def moeq_grouped_mm(x, w, offsets, out=None, stream=None):
+    """Matrix product grouped by expert: ``out[p] = w[e] @ x[p]`` for the rows
+    ``offsets[e] <= p < offsets[e+1]`` of each expert e.  ``x`` bf16
+    ``[M, K]`` sorted by expert, ``w`` bf16 ``[E, N, K]``, ``offsets`` int32
+    ``[E+1]`` on the device (as :func:`moeq_route_buckets` returns them);
+    bf16 ``[M, N]``.  Rows outside ``[offsets[0], offsets[E])`` are not
+    written.  N and K are multiples of 8."""
+    M, E, N, K = _grouped_rows(x, w, offsets, ("x", "K"))
+    if out is not None:
+        _dev(out, torch.bfloat16, "out", (M, N))
+    dev = _on_device("moeq_grouped_mm", x, w, offsets, out)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
+    with _current(dev):
+        _check(_load().moeq_grouped_mm(_ptr(x), _ptr(w), _ptr(offsets), M, E, N, K, _ptr(y), _stream(stream, dev)),
+               "moeq_grouped_mm")
+    if out is None:
+        _used_on(stream, y)
+    return y
+
+
+def moeq_grouped_mm_grad_input(grad_out, w, offsets, grad_x=None, stream=None):
+    """Gradient of :func:`moeq_grouped_mm` with respect to ``x``:
+    ``grad_x[p] = w[e]^T @ grad_out[p]``, bf16 ``[M, K]`` for ``grad_out``
+    bf16 ``[M, N]``.  Rows outside ``[offsets[0], offsets[E])`` are not
+    written."""
+    M, E, N, K = _grouped_rows(grad_out, w, offsets, ("grad_out", "N"))
+    if grad_x is not None:
+        _dev(grad_x, torch.bfloat16, "grad_x", (M, K))
+    dev = _on_device("moeq_grouped_mm_grad_input", grad_out, w, offsets, grad_x)
+    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if grad_x is None else grad_x
+    with _current(dev):
+        _check(_load().moeq_grouped_mm_grad_input(_ptr(grad_out), _ptr(w), _ptr(offsets), M, E, N, K, _ptr(dx),
+                                                  _stream(stream, dev)), "moeq_grouped_mm_grad_input")
+    if grad_x is None:
+        _used_on(stream, dx)
+    return dx
+
+
+def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_w=None, stream=None):
+    """Gradient of :func:`moeq_grouped_mm` with respect to ``w``:
+    ``grad_w[e] = sum_p grad_out[p] x[p]^T`` over the expert's rows (zeros
+    for an expert without rows), ``[E, N, K]`` in fp32 or bf16 (``dtype``, or
+    that of ``grad_w``); the sums are fp32 either way."""
+    for name, t in (("grad_out", grad_out), ("x", x)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{name} must be a 2-D tensor")
+        _dev(t, torch.bfloat16, name)
+    _dev(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must have shape (E + 1,)")
+    (M, N), K, E = grad_out.shape, x.shape[1], offsets.shape[0] - 1
+    if x.shape[0] != M:
+        raise ValueError(f"grad_out has {M} rows and x {x.shape[0]}")
+    if grad_w is not None:
+        dtype = grad_w.dtype if isinstance(grad_w, torch.Tensor) else dtype
+        _dev(grad_w, dtype, "grad_w", (E, N, K))
+    if dtype not in _GRAD_DTYPES:
+        raise TypeError(f"grad_w must be torch.float32 or torch.bfloat16, got {dtype}")
+    dev = _on_device("moeq_grouped_mm_grad_weight", grad_out, x, offsets, grad_w)
+    dw = torch.empty((E, N, K), dtype=dtype, device=dev) if grad_w is None else grad_w
+    with _current(dev):
+        _check(_load().moeq_grouped_mm_grad_weight(_ptr(grad_out), _ptr(x), _ptr(offsets), int(M), int(E), int(N),
+                                                   int(K), _GRAD_DTYPES[dtype], _ptr(dw), _stream(stream, dev)),
+               "moeq_grouped_mm_grad_weight")
+    if grad_w is None:
+        _used_on(stream, dw)
+    return dw
+
+
+def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
+    """:func:`moeq_grouped_mm` with both operands MXFP4 :class:`QWeight`:
+    ``x`` ``[1, M, K]`` (:func:`moeq_quantize_mxfp4` of the sorted rows), ``w``
+    ``[E, N, K]``; bf16 ``[M, N]``.  The scaled products run on the 4-bit
+    matrix instructions with fp32 sums.  N is a multiple of 8."""
+    for name, q in (("x", x), ("w", w)):
+        if not isinstance(q, QWeight):
+            raise TypeError(f"{name} must be a QWeight")
+        if q.format != FMT_MXFP4:
+            raise ValueError(f"{name} has format {q.format}, expected MXFP4 ({FMT_MXFP4})")
+        q.validate_layout()
+    if x.num_experts != 1:
+        raise ValueError(f"x must describe [1, M, K], got {x.shape}")
+    if x.cols != w.cols:
+        raise ValueError(f"x has {x.cols} columns and w {w.cols}")
+    _dev(offsets, torch.int32, "offsets", (w.num_experts + 1,))
+    M, N = x.rows, w.rows
+    if out is not None:
+        _dev(out, torch.bfloat16, "out", (M, N))
+    dev = _on_device("moeq_grouped_mm_mxfp4", *x._tensors(), *w._tensors(), offsets, out)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
+    if M:
+        xc, wc = x._desc(), w._desc()
+        with _current(dev):
+            _check(_load().moeq_grouped_mm_mxfp4(ctypes.byref(xc), ctypes.byref(wc), _ptr(offsets), _ptr(y),
+                                                 _stream(stream, dev)), "moeq_grouped_mm_mxfp4")
+        if out is None:
+            _used_on(stream, y)
+    return y
+
+
+_GRAD_DTYPES = {torch.bfloat16: 1, torch.float32: 2}
+
+
+def moeq_clip_grad_norm_workspace_bytes(count):
+    """Workspace bytes :func:`moeq_clip_grad_norm` needs for ``count`` tensors."""
+    return int(_load().moeq_clip_grad_norm_workspace_bytes(int(count)))
+
+
+def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
+    """The norm over all ``grads`` (bf16 and fp32 tensors of any shape) and
+    ``grad * min(1, max_norm / norm)``, written in place or into ``out`` (one
+    tensor per gradient, of its shape and type).  Returns the norm, an fp32
+    tensor on the device; when it is an infinity or a NaN nothing is scaled.
+    Neither the gradients nor ``out`` may overlap each other."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out must hold {len(grads)} tensors, got {len(outs)}")
+    table = array.array("q")
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not isinstance(g, torch.Tensor):
+            raise TypeError(f"grads[{i}] must be a torch tensor")
+        if g.dtype not in _GRAD_DTYPES:
+            raise TypeError(f"grads[{i}] must be torch.float32 or torch.bfloat16, got {g.dtype}")
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be contiguous")
+        if o is not g:
+            _dev(o, g.dtype, f"out[{i}]", g.shape)
+        table.extend((g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPES[g.dtype]))
+    dev = _on_device("moeq_clip_grad_norm", *grads, *(outs if out is not None else []))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    lib = _load()
+    made = workspace is None
+    workspace = _workspace(workspace, int(lib.moeq_clip_grad_norm_workspace_bytes(len(grads))), dev)
+    with _current(dev):
+        _check(lib.moeq_clip_grad_norm(table.buffer_info()[0], len(grads), float(max_norm), _ptr(norm), _ptr(workspace),
+                                       workspace.numel(), _stream(stream, dev)), "moeq_clip_grad_norm")
+    _used_on(stream, norm, *([workspace] if made else []))
+    return norm

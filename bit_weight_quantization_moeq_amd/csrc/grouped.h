@@ -1,0 +1,37 @@
+// Launchers behind the grouped products, the MXFP4 format and the gradient
+// clipping (their C entry points are in api_grouped.hip).
+#pragma once
+
+#include "moeq_internal.h"
+
+namespace moeq {
+
+hipError_t launch_quantize_mxfp4(const uint16_t* w, uint8_t* q, uint8_t* scales, int64_t nblocks, hipStream_t s);
+hipError_t launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scales, uint16_t* out, int64_t nblocks,
+                                   hipStream_t s);
+
+// One grouped product over rows sorted by expert.
+//   forward:      x [M][kc], w [E][nout][kc], out [M][nout]
+//   grad_input:   x = dy [M][kc], w [E][kc][nout], out = dx [M][nout]
+//   grad_weight:  x [M][kc], w = dy [M][nout], out = dw [E][nout][kc]
+// MXFP4 operands: codes in x / w and one scale byte per 32 values.
+struct GroupedArgs {
+  const void* x;
+  const void* w;
+  const uint8_t* x_scales;
+  const uint8_t* w_scales;
+  const int32_t* offsets;  // [E + 1], on the device
+  void* out;
+  int32_t M, E, nout, kc;
+};
+hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s);
+hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s);
+hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s);
+hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s);
+
+// Gradient clipping.  partial: clip_partials(count) fp64.
+constexpr int kClipPartials = 1024;  // partial sums per launch, at most
+int64_t clip_partials(int32_t count);
+hipError_t launch_clip(const moeq_grad* g, int32_t count, double max_norm, float* norm, double* partial, hipStream_t s);
+
+}  // namespace moeq

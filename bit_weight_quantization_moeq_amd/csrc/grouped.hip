@@ -1,0 +1,507 @@
+// Matrix products grouped by expert over rows sorted by expert (gfx950):
+//
+//   forward       y[p]  = w[e] x[p]                    bf16 or MXFP4 operands
+//   grad_input    dx[p] = w[e]^T dy[p]                 bf16
+//   grad_weight   dw[e] = sum over p of dy[p] x[p]^T   bf16 operands
+//
+// with offsets[e] <= p < offsets[e + 1] the rows of expert e (the layout that
+// moeq_route_buckets and moeq_router_route produce; "MoE Expert
+// Quantization", Axolotl docs, Expert LoRA targeting: adapters and trainable
+// experts beside the frozen packed ones).
+//
+// One kernel body serves the three.  A workgroup owns an output tile: its
+// columns are the MFMA A operand (so a lane ends up with four consecutive
+// output columns of one row) and its rows the B operand.  Each contraction
+// step takes 128 bytes of contraction of every tile row and column through
+// LDS, double-buffered, copied by the LDS DMA of buffer_load ... lds:
+//   * an operand that is contiguous along the contraction (x, w and dy of the
+//     first two products) lies in LDS as rows of 128 B whose 16-B slots are
+//     XOR-swizzled by the row, and is read with ds_read_b128;
+//   * an operand that is contiguous along the output (w in grad_input, both
+//     in grad_weight) lies in LDS as 64 contraction rows of the tile's
+//     columns, and is read with ds_read_b64_tr_b16, which hands each lane of
+//     16 one column of a 4 x 16 block.
+// The buffer resource of a copy ends where the expert's data (or the tile's
+// rows) end, and chunks past the contraction get an offset past that end, so
+// everything out of range arrives in LDS as zeros: rows of the next expert,
+// rows behind the last one and column tails can hold anything.
+//
+// MXFP4: a step of 128 B holds 256 values, eight blocks a row.  The order of
+// the contraction is free as long as both operands agree: MFMA s of a step
+// gives lane half h block 4 h + s of its row, which is 16 B (one LDS slot,
+// as for bf16) and one scale byte, byte s of the dword of scales that the
+// lane holds for the step.  v_mfma_scale_f32_32x32x64_f8f6f4 applies the
+// scales of both operands in the product, with an fp32 sum.
+//
+// offsets are data on the device: they are clamped to [0, M] and no tile
+// leaves the arrays whatever they hold.
+#include "grouped.h"
+
+namespace moeq {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
+
+constexpr int kXcds = 8;
+constexpr int kStepBytes = 128;  // contraction bytes of a row per step
+constexpr int kSub = 4;          // MFMA steps per step
+constexpr int kTileGroup = 4;    // row tiles that run side by side over the column tiles
+constexpr uint32_t kPast = 0x80000000u;  // a buffer offset past every resource's end
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const f32x2 v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Resource of `bytes` bytes at p, with every value in scalar registers.
+__device__ __forceinline__ u32x4 resource(const char* p, int64_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes > 0 ? bytes : 0)), 0x00020000u};
+  return r;
+}
+
+// 16 bytes per lane from resource r at byte off into LDS at lds + 16 * lane;
+// zeros past the resource's end.  Inline assembly (with no register output)
+// so that the compiler does not order later LDS reads behind it: the waits
+// before the barriers do.  The DMA reads M0 one wait state after its write.
+__device__ __forceinline__ void dma16(u32x4 r, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+               : "memory", "m0");
+}
+
+// One operand's side of a tile: kC rows (contraction-contiguous, !kT) or
+// columns (output-contiguous, kT), staged by kNW waves.
+template <bool kT, int kC, int kNW>
+struct Side {
+  static constexpr int kBytes = kC * kStepBytes;
+  static constexpr int kInstr = kC / 8 / kNW;      // DMA instructions per wave per step
+  static constexpr int kLpr = kT ? kC / 8 : 8;     // lanes per LDS row
+  static constexpr int kRpi = 64 / kLpr;           // LDS rows per instruction
+  static constexpr int kPitch = kT ? 2 * kC : kStepBytes;
+  static_assert(kC % (8 * kNW) == 0, "whole instructions per wave");
+  static_assert(!kT || kC == 64 || kC == 128 || kC == 256, "transposed widths");
+
+  // slot swizzle of LDS row r (the same for every row a lane stages)
+  __device__ __forceinline__ static int swz(int r) {
+    if (!kT) return (r >> 1) & 7;   // 16 rows read at one chunk: 16 distinct 16-B banks of 256 B
+    if (kC == 64) return ((r >> 1) & 1) << 2;
+    return (r & 3) << 2;            // 4 rows of 64 B read together: 4 distinct quarters of 256 B
+  }
+
+  const char* base;   // !kT: the tile's first row; kT: the matrix's first row, at the tile's first column
+  int64_t bytes;      // from base to the end of what may be read
+  int32_t stride;     // bytes per row
+  int32_t kbytes;     // !kT: contraction bytes of a row
+  uint32_t voff;      // lane's offset of instruction 0
+  int32_t chunk16;    // byte of the lane's chunk within its row
+
+  __device__ __forceinline__ void init(const void* p, int64_t size, int32_t stride_, int32_t kbytes_, int wave, int lane) {
+    base = static_cast<const char*>(p);
+    bytes = size;
+    stride = stride_;
+    kbytes = kbytes_;
+    const int r = kRpi * wave + lane / kLpr;
+    chunk16 = 16 * ((lane % kLpr) ^ swz(r));
+    voff = (uint32_t)r * (uint32_t)stride + (uint32_t)chunk16;
+  }
+  // resource of step ks
+  __device__ __forceinline__ u32x4 step(int ks) const {
+    if (!kT) return resource(base, bytes);
+    const int64_t skip = (int64_t)ks * 64 * stride;
+    const int64_t left = bytes - skip;
+    const int64_t most = (int64_t)64 * stride;
+    return resource(base + skip, left < most ? left : most);
+  }
+  // instruction i of step ks into the LDS tile at lds
+  __device__ __forceinline__ void dma(u32x4 r, int ks, int i, int wave, uint32_t lds) const {
+    uint32_t off = voff + (uint32_t)(i * kRpi * kNW) * (uint32_t)stride;
+    if (!kT) {
+      off += (uint32_t)ks * kStepBytes;
+      off = ks * kStepBytes + chunk16 < kbytes ? off : kPast;
+    }
+    dma16(r, off, lds + (uint32_t)(i * kNW + wave) * 1024u);
+  }
+  // Operand fragment of the 32 rows / columns from c0 on at MFMA step s:
+  // lane (l32, h) gets contraction chunk 4 h + s (8 bf16, or one MXFP4 block).
+  __device__ __forceinline__ static u32x4 frag(const char* tile, int c0, int s, int lane) {
+    const int l32 = lane & 31, h = lane >> 5;
+    if constexpr (!kT) {
+      const int slot = (4 * h + s) ^ swz(l32);
+      return *reinterpret_cast<const u32x4*>(tile + (c0 + l32) * kStepBytes + 16 * slot);
+    } else {
+      const int L = lane & 15, g = (lane >> 4) & 1;
+      const int r = 8 * (4 * h + s) + (L >> 2);
+      const int slot = (c0 / 8 + 2 * g + ((L & 3) >> 1)) ^ swz(L >> 2);
+      const char* p = tile + r * kPitch + 16 * slot + 8 * (L & 1);
+      const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p)));
+      const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * kPitch)));
+      return u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
+  }
+};
+
+// Scale bytes of MXFP4 rows: eight per row and step.
+struct ScaleRow {
+  const uint8_t* p;  // the row's scales, or nullptr past the tile
+  int32_t n;         // scales per row
+  __device__ __forceinline__ uint2 load(int ks) const {
+    uint2 v = make_uint2(0u, 0u);
+    if (!p) return v;
+    const int at = 8 * ks;
+    if (at + 8 <= n) {
+      __builtin_memcpy(&v, p + at, 8);
+    } else {
+      uint64_t b = 0;
+      for (int i = 0; at + i < n; ++i) b |= (uint64_t)p[at + i] << (8 * i);
+      v = make_uint2((uint32_t)b, (uint32_t)(b >> 32));
+    }
+    return v;
+  }
+};
+
+// Shape of a tile: kNWN x kNWM waves, each kTN blocks of 32 columns by kTM
+// blocks of 32 rows.
+template <bool kMX, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM>
+struct Tile {
+  static constexpr int kNW = kNWN * kNWM;
+  static constexpr int kCols = 32 * kTN * kNWN, kRows = 32 * kTM * kNWM;
+  using A = Side<kAT, kCols, kNW>;
+  using B = Side<kBT, kRows, kNW>;
+  static constexpr int kBuf = A::kBytes + B::kBytes;
+  static constexpr int kScaleBuf = kMX ? 8 * (kCols + kRows) : 0;
+  static constexpr int kInstr = A::kInstr + B::kInstr;
+
+  // acc[n][m]: 32 columns x 32 rows each
+  __device__ __forceinline__ static void run(char* smem, const A& a, const B& b, ScaleRow sr, int nks,
+                                             f32x16 (&acc)[kTN][kTM]) {
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wn = wave % kNWN, wm = wave / kNWN;
+    uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
+    asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
+    char* sc = smem + 2 * kBuf;     // MX: scales, kCols then kRows rows of 8 B, two buffers
+
+    u32x4 ra, rb;
+    auto dma = [&](int ks, int buf, int i) {
+      const uint32_t l = lds0 + (uint32_t)buf * kBuf;
+      if (i < A::kInstr)
+        a.dma(ra, ks, i, wave, l);
+      else
+        b.dma(rb, ks, i - A::kInstr, wave, l + A::kBytes);
+    };
+    auto scale_store = [&](int buf, uint2 v) {
+      if (t < kCols + kRows) *reinterpret_cast<uint2*>(sc + buf * kScaleBuf + 8 * t) = v;
+    };
+    auto frags = [&](const char* buf, int s, u32x4 (&fa)[kTN], u32x4 (&fb)[kTM]) {
+#pragma unroll
+      for (int n = 0; n < kTN; ++n) fa[n] = A::frag(buf, 32 * (kTN * wn + n), s, lane);
+#pragma unroll
+      for (int m = 0; m < kTM; ++m) fb[m] = B::frag(buf + A::kBytes, 32 * (kTM * wm + m), s, lane);
+    };
+
+    ra = a.step(0);
+    rb = b.step(0);
+#pragma unroll
+    for (int i = 0; i < kInstr; ++i) dma(0, 0, i);
+    if constexpr (kMX) scale_store(0, sr.load(0));
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+
+    for (int ks = 0; ks < nks; ++ks) {
+      const int buf = ks & 1;
+      const char* tile = smem + buf * kBuf;
+      uint2 sv = make_uint2(0u, 0u);
+      uint32_t sa[kTN], sb[kTM];
+      if constexpr (kMX) {
+        if (ks + 1 < nks) sv = sr.load(ks + 1);
+        const char* s0 = sc + buf * kScaleBuf + 8 * (lane & 31) + 4 * (lane >> 5);
+#pragma unroll
+        for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
+#pragma unroll
+        for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
+      }
+      ra = a.step(ks + 1);  // (past the last step everything is out of range)
+      rb = b.step(ks + 1);
+      u32x4 fa[2][kTN], fb[2][kTM];
+      frags(tile, 0, fa[0], fb[0]);
+#pragma unroll
+      for (int s = 0; s < kSub; ++s) {
+        if (s + 1 < kSub) frags(tile, s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
+        // the next step's copies, in the first three quarters of this one
+#pragma unroll
+        for (int i = s * kInstr / (kSub - 1); i < (s + 1) * kInstr / (kSub - 1) && i < kInstr; ++i)
+          dma(ks + 1, buf ^ 1, i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kTN; ++n)
+#pragma unroll
+          for (int m = 0; m < kTM; ++m) {
+            if constexpr (kMX) {
+              const u32x4 x = fa[s & 1][n], y = fb[s & 1][m];
+              const i32x8 xa = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
+              const i32x8 yb = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
+              // operand formats 4: E2M1; scale byte s of the lanes' dwords
+              if (s == 0)
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 0, sa[n], 0, sb[m]);
+              else if (s == 1)
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 1, sa[n], 1, sb[m]);
+              else if (s == 2)
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 2, sa[n], 2, sb[m]);
+              else
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 3, sa[n], 3, sb[m]);
+            } else {
+              acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fa[s & 1][n]),
+                                                                  __builtin_bit_cast(bf16x8, fb[s & 1][m]),
+                                                                  acc[n][m], 0, 0, 0);
+            }
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (kMX) scale_store(buf ^ 1, sv);
+      // Every copy of the next step has landed and every LDS access of this
+      // one is done before any wave goes on.
+      __builtin_amdgcn_s_waitcnt(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    }
+  }
+
+  // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
+  // out, ld elements a row, staged through LDS so that the stores write whole
+  // rows (from the accumulator layout one instruction would touch 32 rows).
+  // Fp32 tiles go by the rows of one row of waves at a time.
+  template <typename T>
+  __device__ __forceinline__ static void store(char* smem, const f32x16 (&acc)[kTN][kTM], T* out, int64_t ld, int nrows,
+                                               int ncols) {
+    constexpr int kPer = 16 / (int)sizeof(T);
+    constexpr int kPasses = sizeof(T) == 4 ? kNWM : 1;
+    constexpr int kPassRows = kRows / kPasses;
+    constexpr int kOutPitch = kCols * (int)sizeof(T) + 16;
+    constexpr int kChunks = kCols / kPer;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int wn = wave % kNWN, wm = wave / kNWN, l32 = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int pass = 0; pass < kPasses; ++pass) {
+      if (pass) __syncthreads();
+      if (kPasses == 1 || wm == pass) {
+#pragma unroll
+        for (int m = 0; m < kTM; ++m) {
+          const int r = 32 * ((kPasses == 1 ? kTM * wm : 0) + m) + l32;
+#pragma unroll
+          for (int n = 0; n < kTN; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              char* p = smem + r * kOutPitch + (int)sizeof(T) * (32 * (kTN * wn + n) + 8 * q + 4 * h);
+              const f32x16& v = acc[n][m];
+              if constexpr (sizeof(T) == 4)
+                *reinterpret_cast<float4*>(p) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+              else
+                *reinterpret_cast<uint2*>(p) =
+                    make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+            }
+        }
+      }
+      __syncthreads();
+      const int first = pass * kPassRows;
+      for (int c = t; c < kPassRows * kChunks; c += 64 * kNW) {
+        const int r = c / kChunks, k = c % kChunks;
+        if (first + r < nrows && kPer * k < ncols)
+          *reinterpret_cast<uint4*>(out + (int64_t)(first + r) * ld + kPer * k) =
+              *reinterpret_cast<const uint4*>(smem + r * kOutPitch + 16 * k);
+      }
+    }
+  }
+  static constexpr int out_bytes(int size) { return (size == 4 ? kRows / kNWM : kRows) * (kCols * size + 16); }
+};
+
+constexpr int imax(int a, int b) { return a > b ? a : b; }
+
+// Rows [lo, hi) of expert e, in range whatever offsets hold.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int M, int& lo, int& n) {
+  lo = min(max(offsets[e], 0), M);
+  n = max(min(offsets[e + 1], M) - lo, 0);
+}
+
+// Work item of this workgroup among the (expert, row tile, column tile)
+// triples, expert-major; every XCD takes a contiguous range, so that the
+// tiles that share an expert's weights and rows share an L2.  An expert's
+// rows are cut into ceil(rows / max_rows) near-equal tiles, taken in groups
+// of kTileGroup that go through the column tiles together.  Each wave scans
+// the experts by itself, 64 at a time.
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int max_rows, int ncol, int& e, int& row0,
+                                          int& nrows, int& ct) {
+  const int lane = threadIdx.x & 63;
+  auto tiles = [&](int i, int& lo, int& n) {
+    lo = n = 0;
+    if (i < E) expert_rows(offsets, i, M, lo, n);
+    return (n + max_rows - 1) / max_rows;
+  };
+  int lo, n, total = 0;
+  for (int i = 0; i < E; i += 64) total += tiles(i + lane, lo, n);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o, 64);
+  total = __builtin_amdgcn_readfirstlane(total) * ncol;
+  const int per = (total + kXcds - 1) / kXcds;
+  const int slot = blockIdx.x / kXcds, w = (blockIdx.x % kXcds) * per + slot;
+  if (slot >= per || w >= total) return false;
+  int before = 0;
+  for (int i = 0; i < E; i += 64) {
+    const int nt = tiles(i + lane, lo, n);
+    int incl = nt;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += v;
+    }
+    const int first = before + incl - nt;
+    const uint64_t hit = __ballot(w >= first * ncol && w < (first + nt) * ncol);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      e = i + src;
+      const int f = __builtin_amdgcn_readlane(first, src), k = __builtin_amdgcn_readlane(nt, src);
+      const int r0 = __builtin_amdgcn_readlane(lo, src), c = __builtin_amdgcn_readlane(n, src);
+      const int r = w - f * ncol, g = r / (kTileGroup * ncol), gt = min(kTileGroup, k - g * kTileGroup);
+      const int rr = r - g * kTileGroup * ncol;
+      ct = rr / gt;
+      const int mt = g * kTileGroup + (rr - ct * gt);
+      const int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
+      row0 = r0 + a;
+      nrows = b - a;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// forward (kAT = false, kMX or not) and grad_input (kAT = true).
+//   x [M][kc], w [E][..], out [M][nout]: kc contraction length, nout columns.
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM>
+__device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int e, int row0, int nrows, int c0) {
+  using T = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM>;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
+  typename T::A a;
+  typename T::B b;
+  const char* w = static_cast<const char*>(g.w);
+  const int ncols = min(T::kCols, g.nout - c0);
+  if constexpr (kAT) {
+    const int64_t expert = (int64_t)g.kc * g.nout * 2;
+    a.init(w + e * expert + 2 * c0, expert - 2 * c0, 2 * g.nout, 0, wave, lane);
+  } else {
+    a.init(w + ((int64_t)e * g.nout + c0) * kbytes, (int64_t)ncols * kbytes, kbytes, kbytes, wave, lane);
+  }
+  b.init(static_cast<const char*>(g.x) + (int64_t)row0 * kbytes, (int64_t)nrows * kbytes, kbytes, kbytes, wave, lane);
+  ScaleRow sr = {nullptr, g.kc / 32};
+  if constexpr (kMX) {
+    if (t < T::kCols) {
+      if (t < ncols) sr.p = g.w_scales + ((int64_t)e * g.nout + c0 + t) * sr.n;
+    } else if (t - T::kCols < nrows) {
+      sr.p = g.x_scales + (int64_t)(row0 + t - T::kCols) * sr.n;
+    }
+  }
+  f32x16 acc[kTN][kTM];
+#pragma unroll
+  for (int n = 0; n < kTN; ++n)
+#pragma unroll
+    for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
+  T::run(smem, a, b, sr, (kbytes + kStepBytes - 1) / kStepBytes, acc);
+  T::store(smem, acc, static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.nout + c0, g.nout, nrows, ncols);
+}
+
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN>
+__global__ __launch_bounds__(64 * kNWN * kNWM, 2) void rows_kernel(GroupedArgs g) {
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, 4>;
+  __shared__ __attribute__((aligned(16))) char smem[imax(2 * Big::kBuf + 2 * Big::kScaleBuf, Big::out_bytes(2))];
+  int e, row0, nrows, ct;
+  if (!find_tile(g.offsets, g.E, g.M, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
+  const int c0 = ct * Big::kCols;
+  // blocks of 32 rows per wave: as few as the tile's rows need
+  if (nrows > 3 * 32 * kNWM)
+    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 4>(smem, g, e, row0, nrows, c0);
+  else if (nrows > 2 * 32 * kNWM)
+    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 3>(smem, g, e, row0, nrows, c0);
+  else if (nrows > 32 * kNWM)
+    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 2>(smem, g, e, row0, nrows, c0);
+  else
+    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1>(smem, g, e, row0, nrows, c0);
+}
+
+// grad_weight: tile of dw[e] [N][K]: rows n (dy columns, B), columns k (x
+// columns, A), contraction over the expert's rows.
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM>
+__global__ __launch_bounds__(64 * kNWN * kNWM, 2) void weight_kernel(GroupedArgs g) {
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM>;
+  __shared__ __attribute__((aligned(16))) char smem[imax(2 * T::kBuf, T::out_bytes(sizeof(Out)))];
+  const int N = g.nout, K = g.kc;
+  const int nk = (K + T::kCols - 1) / T::kCols, nn = (N + T::kRows - 1) / T::kRows;
+  const int total = g.E * nn * nk, per = (total + kXcds - 1) / kXcds;
+  const int slot = blockIdx.x / kXcds, w = (blockIdx.x % kXcds) * per + slot;
+  if (slot >= per || w >= total) return;
+  const int e = w / (nn * nk), r = w - e * nn * nk;
+  // row tiles in groups, as in find_tile
+  const int grp = r / (kTileGroup * nk), gt = min(kTileGroup, nn - grp * kTileGroup), rr = r - grp * kTileGroup * nk;
+  const int k0 = (rr / gt) * T::kCols, n0 = (grp * kTileGroup + rr % gt) * T::kRows;
+  int lo, cnt;
+  expert_rows(g.offsets, e, g.M, lo, cnt);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  cnt = __builtin_amdgcn_readfirstlane(cnt);
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  typename T::A a;
+  typename T::B b;
+  a.init(static_cast<const char*>(g.x) + ((int64_t)lo * K + k0) * 2, (int64_t)cnt * K * 2 - 2 * k0, 2 * K, 0, wave, lane);
+  b.init(static_cast<const char*>(g.w) + ((int64_t)lo * N + n0) * 2, (int64_t)cnt * N * 2 - 2 * n0, 2 * N, 0, wave, lane);
+  f32x16 acc[kTN][kTM];
+#pragma unroll
+  for (int n = 0; n < kTN; ++n)
+#pragma unroll
+    for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
+  T::run(smem, a, b, ScaleRow{nullptr, 0}, (cnt + 63) / 64, acc);
+  T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)e * N + n0) * K + k0, K, min(T::kRows, N - n0),
+           min(T::kCols, K - k0));
+}
+
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN>
+hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, 4>;
+  const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
+  const int64_t tiles = (int64_t)g.M / Big::kRows + (g.E < g.M ? g.E : g.M);
+  const int64_t grid = (tiles * ncol + kXcds - 1) / kXcds * kXcds;
+  rows_kernel<kMX, kAT, kNWN, kNWM, kTN><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM>
+hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM>;
+  const int64_t total = (int64_t)g.E * ((g.nout + T::kRows - 1) / T::kRows) * ((g.kc + T::kCols - 1) / T::kCols);
+  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
+  weight_kernel<Out, kNWN, kNWM, kTN, kTM><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) { return launch_rows<false, false, 4, 2, 2>(g, s); }
+
+hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) { return launch_rows<true, false, 4, 2, 2>(g, s); }
+
+hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
+  return launch_rows<false, true, 4, 2, 2>(g, s);
+}
+
+hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
+  return fp32 ? launch_weight<float, 4, 2, 2, 4>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4>(g, s);
+}
+
+}  // namespace moeq

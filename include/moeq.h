@@ -34,6 +34,7 @@ extern "C" {
 #define MOEQ_ABI_VERSION 3
 #define MOEQ_NF4_BLOCKSIZE 64
 #define MOEQ_DQ_GROUP 256 /* NF4 blocks per double-quantization group */
+#define MOEQ_MXFP4_BLOCKSIZE 32
 #define MOEQ_MAX_EXPERTS 1024
 
 typedef int32_t moeq_status;
@@ -49,7 +50,10 @@ enum {
   MOEQ_EDEVICE = -7     /* a HIP call failed                                         */
 };
 
-enum { MOEQ_FMT_NF4 = 1, MOEQ_FMT_INT8_ROWWISE = 2, MOEQ_FMT_NF4_DQ = 3 };
+enum { MOEQ_FMT_NF4 = 1, MOEQ_FMT_INT8_ROWWISE = 2, MOEQ_FMT_NF4_DQ = 3, MOEQ_FMT_MXFP4 = 4 };
+
+/* Element types of gradients. */
+enum { MOEQ_DTYPE_BF16 = 1, MOEQ_DTYPE_FP32 = 2 };
 
 /*
  * A quantized expert tensor [E][rows][cols] in caller-owned device memory.
@@ -80,9 +84,21 @@ enum { MOEQ_FMT_NF4 = 1, MOEQ_FMT_INT8_ROWWISE = 2, MOEQ_FMT_NF4_DQ = 3 };
  *                consecutive blocks of one expert, the last one possibly
  *                shorter; an all-zero group stores s2 = 0 and codes 0).
  *   The weights decode with absmax' = fp32(c * s2).
+ * MXFP4 (format MOEQ_FMT_MXFP4, blocksize 32; the microscaled 4-bit floating
+ * point of the OCP Microscaling specification):
+ *   qdata        uint8 [E][rows][cols/2]: E2M1 codes (sign, two exponent bits,
+ *                one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 in magnitude);
+ *                column 2m in the LOW nibble of byte m, column 2m+1 in the
+ *                high nibble.
+ *   scale_codes  uint8 [E][rows*cols/32]: one byte s per block of 32 columns,
+ *                the scale 2^(s - 127); s = 255 makes the whole block NaN.
+ *   scales       NULL.
  * Since blocks and groups never straddle an expert, &qdata[e] / &scales[e]
  * (and &scale_codes[e]) with num_experts = 1 describe expert e alone.
- * scale_codes must be NULL for the other formats.
+ * scale_codes must be NULL for plain NF4 and int8.
+ * The experts and offload calls below take NF4, NF4_DQ and int8 tensors;
+ * MXFP4 tensors belong to the calls that name the format, and any other call
+ * returns MOEQ_EFORMAT.
  */
 typedef struct moeq_qweight {
   int32_t format;
@@ -403,6 +419,93 @@ size_t moeq_route_workspace_bytes(int32_t T, int32_t K, int32_t E);
 moeq_status moeq_route_buckets(const int32_t *top_k_index, int32_t T, int32_t K, int32_t E,
                                int32_t *counts, int32_t *offsets, int32_t *perm, int32_t *slot,
                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Quantize to MXFP4: w_bf16 bf16 [E][rows][cols] (16-byte aligned; weights,
+ * or activations with E = 1); dst format MOEQ_FMT_MXFP4, blocksize 32,
+ * cols % 32 == 0, 16-byte aligned qdata and scale_codes.  For each block of
+ * 32 columns: s = max(floor(log2(max |w|)) - 2, -127) + 127, code = the E2M1
+ * value nearest to w * 2^(127 - s), ties to the even code, at most 6 in
+ * magnitude; an all-zero block stores s = 0 and zero codes.  A block with an
+ * infinity or a NaN stores s = 255 (NaN) and zero codes.
+ */
+moeq_status moeq_quantize_mxfp4(const uint16_t *w_bf16, const moeq_qweight *dst, void *stream);
+
+/*
+ * MXFP4 -> bf16 [E][rows][cols], 16-byte aligned: E2M1 value * 2^(s - 127),
+ * exact (s >= 253, which moeq_quantize_mxfp4 never writes, can overflow to
+ * infinities); NaN for s = 255.
+ */
+moeq_status moeq_dequantize_mxfp4(const moeq_qweight *src, uint16_t *out_bf16, void *stream);
+
+/*
+ * Matrix products grouped by expert, for rows sorted by expert: what trains
+ * or serves expert weights and per-expert adapters in bf16 beside the packed
+ * ones ("MoE Expert Quantization", Axolotl docs, Expert LoRA targeting).
+ * Rows p with offsets[e] <= p < offsets[e + 1] belong to expert e:
+ *   moeq_grouped_mm              out[p] = w[e] x[p]
+ *   moeq_grouped_mm_grad_input   grad_x[p] = w[e]^T grad_out[p]
+ *   moeq_grouped_mm_grad_weight  grad_w[e] = sum over p of grad_out[p] x[p]^T
+ *   x, grad_x      bf16 [M][K]
+ *   w              bf16 [E][N][K]
+ *   out, grad_out  bf16 [M][N]
+ *   grad_w         fp32 (dtype MOEQ_DTYPE_FP32) or bf16 (MOEQ_DTYPE_BF16)
+ *                  [E][N][K]; zeros for an expert without rows
+ *   offsets        int32 [E+1] on the device, ascending, as
+ *                  moeq_route_buckets and moeq_router_route write them
+ * Products of bf16 values summed in fp32, rounded once at the end; the same
+ * bits from run to run.  Rows of out and grad_x outside [offsets[0],
+ * offsets[E]) are not written, and rows outside an expert's range never
+ * reach its results (they may hold anything).  Offsets are clamped to
+ * [0, M]; ones that do not ascend give undefined results, but no access
+ * outside the arrays.  Every pointer 16-byte aligned, except offsets.
+ * MOEQ_ESHAPE unless N and K are multiples of 8 of at most 2^20, N*K*2 < 2^31,
+ * E <= MOEQ_MAX_EXPERTS and M <= 2^28.  M == 0 is a valid no-op, except that
+ * moeq_grouped_mm_grad_weight then writes zeros.
+ */
+moeq_status moeq_grouped_mm(const uint16_t *x_bf16, const uint16_t *w_bf16, const int32_t *offsets, int32_t M,
+                            int32_t E, int32_t N, int32_t K, uint16_t *out_bf16, void *stream);
+moeq_status moeq_grouped_mm_grad_input(const uint16_t *grad_out_bf16, const uint16_t *w_bf16, const int32_t *offsets,
+                                       int32_t M, int32_t E, int32_t N, int32_t K, uint16_t *grad_x_bf16,
+                                       void *stream);
+moeq_status moeq_grouped_mm_grad_weight(const uint16_t *grad_out_bf16, const uint16_t *x_bf16, const int32_t *offsets,
+                                        int32_t M, int32_t E, int32_t N, int32_t K, int32_t dtype, void *grad_w,
+                                        void *stream);
+
+/*
+ * moeq_grouped_mm with both operands in MXFP4: x one "expert" of M rows
+ * ([1][M][K], activations quantized with moeq_quantize_mxfp4), w [E][N][K].
+ * The block scales are applied inside the matrix instructions; products are
+ * summed in fp32 and rounded once to bf16.  A NaN block makes the outputs
+ * that it enters NaN.  Otherwise as moeq_grouped_mm, with K % 32 == 0.
+ */
+moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, const int32_t *offsets,
+                                  uint16_t *out_bf16, void *stream);
+
+/*
+ * The norm of all gradients of a training step, and their clipping:
+ *   *norm = sqrt(sum of squares over every tensor)
+ *   dst   = src * min(1, max_norm / *norm), in the tensor's own type
+ * grads is a HOST array of `count` descriptors (read before the call
+ * returns; src and dst are device memory).  dst == src clips in place; a dst
+ * elsewhere must overlap no src and no other dst (MOEQ_EINVAL).  src and dst
+ * are aligned to their type.  norm: one fp32 on the device.  The sum is
+ * formed in fp64 in a fixed order: the same bits from run to run, and no
+ * overflow.  A norm that is an infinity or a NaN scales nothing (dst becomes
+ * src), so that the caller can skip the step on *norm alone.  Empty tensors are allowed; count
+ * == 0 gives a norm of 0.  MOEQ_EINVAL for a max_norm that is negative or
+ * NaN.  Workspace of moeq_clip_grad_norm_workspace_bytes(count), 16-byte
+ * aligned.
+ */
+typedef struct moeq_grad {
+  const void *src;
+  void *dst;
+  int64_t numel;
+  int32_t dtype; /* MOEQ_DTYPE_BF16 or MOEQ_DTYPE_FP32 */
+} moeq_grad;
+size_t moeq_clip_grad_norm_workspace_bytes(int32_t count);
+moeq_status moeq_clip_grad_norm(const moeq_grad *grads, int32_t count, double max_norm, float *norm, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -40,6 +40,8 @@ Modules:
 * :mod:`oracle.router`  -- the router front-end (logits, softmax, top-K) in fp64.
 * :mod:`oracle.dq`      -- double quantization of the NF4 absmax (8-bit codes
   per 256-block group of one expert, fp32 group scales).
+* :mod:`oracle.mxfp4`   -- MXFP4 quantize, dequantize.
+* :mod:`oracle.grouped` -- products grouped by expert and their gradients.
 
 Parity status: every function here is pinned by ``tests/test_oracle_*.py``
 against closed forms, brute force, exact rational arithmetic or library
