@@ -139,7 +139,7 @@ moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight* x, const moeq_qweight* w, 
 }
 
 size_t moeq_clip_grad_norm_workspace_bytes(int32_t count) {
-  return count < 0 ? 0 : sizeof(double) * (size_t)clip_partials(count);
+  return count < 0 ? 0 : sizeof(double) * (size_t)(kClipHead + clip_partials(count));
 }
 
 moeq_status moeq_clip_grad_norm(const moeq_grad* grads, int32_t count, double max_norm, float* norm, void* workspace,
@@ -148,15 +148,15 @@ moeq_status moeq_clip_grad_norm(const moeq_grad* grads, int32_t count, double ma
   if (!(max_norm >= 0.0)) return MOEQ_EINVAL;
   for (int32_t i = 0; i < count; ++i) {
     const moeq_grad& g = grads[i];
-    if (g.numel < 0 || g.numel > (int64_t(1) << 48) || (g.numel > 0 && (!g.src || !g.dst))) return MOEQ_EINVAL;
+    if (g.numel < 0 || g.numel > (int64_t(1) << 37) || (g.numel > 0 && (!g.src || !g.dst))) return MOEQ_EINVAL;
     if (g.dtype != MOEQ_DTYPE_BF16 && g.dtype != MOEQ_DTYPE_FP32) return MOEQ_EFORMAT;
     const uintptr_t size = g.dtype == MOEQ_DTYPE_FP32 ? 4 : 2;
     if (g.numel > 0 && (reinterpret_cast<uintptr_t>(g.src) % size || reinterpret_cast<uintptr_t>(g.dst) % size))
       return MOEQ_EALIGN;
   }
   if (reinterpret_cast<uintptr_t>(norm) % 4) return MOEQ_EALIGN;
-  if (count > 0 && (!workspace || workspace_bytes < moeq_clip_grad_norm_workspace_bytes(count))) return MOEQ_EWORKSPACE;
-  if (count > 0 && !aligned16(workspace)) return MOEQ_EALIGN;
+  if (!workspace || workspace_bytes < moeq_clip_grad_norm_workspace_bytes(count)) return MOEQ_EWORKSPACE;
+  if (!aligned16(workspace)) return MOEQ_EALIGN;
   try {
     if (overlapping(grads, count)) return MOEQ_EINVAL;
   } catch (const std::bad_alloc&) {

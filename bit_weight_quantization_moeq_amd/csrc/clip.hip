@@ -5,13 +5,13 @@
 //
 // for any number of bf16 and fp32 tensors ("MoE Expert Quantization", Axolotl
 // docs, Expert LoRA targeting: adapters and routers train beside the frozen
-// experts).  Two passes over the data, both bound by HBM, in one launch each
-// per kTable tensors:
-//   sum_kernel    every workgroup adds the squares of its chunks (a chunk lies
-//                 in one tensor) in fp64 and writes one partial sum;
-//   scale_kernel  every workgroup adds all partial sums in the same fixed
-//                 order (at most a few thousand, from L2), so all of them and
-//                 every run get the same norm bits, then scales its chunks.
+// experts).  Two passes over the data, both bound by HBM, each in one launch
+// per kTable tensors, with a small kernel between them:
+//   sum_kernel    adds the squares of its chunks (a chunk lies in one tensor)
+//                 in fp64; one partial sum per workgroup;
+//   norm_kernel   one workgroup adds the partial sums in a fixed order and
+//                 leaves the norm and the factor;
+//   scale_kernel  one workgroup per chunk.
 // A square of an fp32 or bf16 value is exact in fp64 and cannot overflow it,
 // so the norm is right to fp32 for every finite gradient.
 //
@@ -22,10 +22,16 @@
 namespace moeq {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4a __attribute__((aligned(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kThreads = 256;
 constexpr int kTable = 96;            // tensors per launch (the kernel arguments hold the table)
 constexpr int kMaxGrid = kClipPartials;
-constexpr int64_t kChunk = 1 << 14;   // elements per chunk
+constexpr int kUnroll = 8;             // 16-byte vectors of a thread in flight
+constexpr int64_t kChunkBytes = 16 * kThreads * kUnroll;
 
 struct Entry {
   const void* src;
@@ -42,22 +48,81 @@ struct Table {
 
 __device__ __forceinline__ bool is_fp32(const Table& t, int i) { return (t.fp32[i >> 5] >> (i & 31)) & 1u; }
 
-// Tensor that holds chunk c.
+// elements per chunk
+__host__ __device__ __forceinline__ int64_t chunk_of(bool fp32) { return kChunkBytes / (fp32 ? 4 : 2); }
+
+// Tensor that holds chunk c: the lanes look at all of the table at once.
 __device__ __forceinline__ int tensor_of(const Table& t, int64_t c) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.e[mid].first <= c) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kTable; i += 64)
+    n += __popcll(__ballot(i + lane < t.count && t.e[min(i + lane, kTable - 1)].first <= c));
+  return __builtin_amdgcn_readfirstlane(n - 1);
 }
 
-__device__ __forceinline__ float get(const uint16_t* p, int64_t i) { return __uint_as_float((uint32_t)p[i] << 16); }
-__device__ __forceinline__ float get(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ void put(uint16_t* p, int64_t i, float v) {
-  p[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
+// 16 bytes of a tensor as fp32 and back.  Tensors are aligned to their
+// elements only; the hardware takes 16-byte accesses at any address.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void unpack(const u32x4& v, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[4]) {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+  }
+};
+template <>
+struct Vec<uint16_t> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const u32x4& v, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ u32x4 pack(const float (&f)[8]) {
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 p = {f[2 * i], f[2 * i + 1]};
+      v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+    }
+    return v;
+  }
+};
+__device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ void from_float(float v, uint16_t& o) { o = __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ void from_float(float v, float& o) { o = v; }
+
+// Calls vec(u, i) for the n / kN whole vectors of a chunk, kUnroll at a time
+// with all their loads first, and one(i) for the elements behind them.
+template <typename T, typename V, typename O>
+__device__ __forceinline__ void each(const T* p, int n, V vec, O one) {
+  constexpr int kN = Vec<T>::kN;
+  const int nv = n / kN;
+  int i = threadIdx.x;
+  for (; i + (kUnroll - 1) * kThreads < nv; i += kUnroll * kThreads) {
+    u32x4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4a*>(p + (int64_t)(i + u * kThreads) * kN));
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) vec(v[u], i + u * kThreads);
+  }
+  for (; i < nv; i += kThreads) {
+    u32x4 v;
+    __builtin_memcpy(&v, p + (int64_t)i * kN, 16);
+    vec(v, i);
+  }
+  const int r = nv * kN + (int)threadIdx.x;
+  if (r < n) one(r);
 }
-__device__ __forceinline__ void put(float* p, int64_t i, float v) { p[i] = v; }
 
 // Sum over the workgroup, in a fixed order; every thread gets it.
 __device__ __forceinline__ double block_sum(double v) {
@@ -74,12 +139,20 @@ __device__ __forceinline__ double block_sum(double v) {
 }
 
 template <typename T>
-__device__ __forceinline__ double chunk_squares(const T* p, int64_t n) {
+__device__ __forceinline__ double chunk_squares(const T* p, int n) {
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-    const double g = (double)get(p, i);
-    s += g * g;
-  }
+  each(
+      p, n,
+      [&](const u32x4& v, int) {
+        float f[Vec<T>::kN];
+        Vec<T>::unpack(v, f);
+#pragma unroll
+        for (int k = 0; k < Vec<T>::kN; ++k) s = __builtin_fma((double)f[k], (double)f[k], s);
+      },
+      [&](int i) {
+        const double g = (double)to_float(p[i]);
+        s = __builtin_fma(g, g, s);
+      });
   return s;
 }
 
@@ -87,7 +160,8 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(Table t, double* __restri
   double s = 0.0;
   for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int i = tensor_of(t, c);
-    const int64_t at = (c - t.e[i].first) * kChunk, n = min(kChunk, t.e[i].n - at);
+    const int64_t chunk = chunk_of(is_fp32(t, i)), at = (c - t.e[i].first) * chunk;
+    const int n = (int)min(chunk, t.e[i].n - at);
     s += is_fp32(t, i) ? chunk_squares(static_cast<const float*>(t.e[i].src) + at, n)
                        : chunk_squares(static_cast<const uint16_t*>(t.e[i].src) + at, n);
   }
@@ -96,28 +170,46 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(Table t, double* __restri
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int64_t n, float k) {
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) put(dst, i, get(src, i) * k);
+__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, float k) {
+  each(
+      src, n,
+      [&](const u32x4& v, int i) {
+        float f[Vec<T>::kN];
+        Vec<T>::unpack(v, f);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::kN; ++j) f[j] *= k;
+        const u32x4 o = Vec<T>::pack(f);
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4a*>(dst + (int64_t)i * Vec<T>::kN));
+      },
+      [&](int i) { from_float(to_float(src[i]) * k, dst[i]); });
 }
 
-__global__ __launch_bounds__(kThreads) void scale_kernel(Table t, const double* __restrict__ partial, int32_t partials,
-                                                        double max_norm, float* __restrict__ norm_out) {
+// The norm and the factor of every gradient: 1 when there is nothing to clip,
+// also for a norm that is no finite number.
+__global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ partial, int32_t partials,
+                                                       double max_norm, float* __restrict__ norm_out,
+                                                       float* __restrict__ factor) {
   double s = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) s += partial[i];
   const double norm = sqrt(block_sum(s));
-  if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  // a norm that is no finite number scales nothing
-  const bool clip = norm > max_norm && norm < __builtin_inf();
-  const float k = clip ? (float)(max_norm / norm) : 1.0f;
-  for (int64_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    if (!clip && t.e[i].src == t.e[i].dst) continue;  // nothing to change in place
-    const int64_t at = (c - t.e[i].first) * kChunk, n = min(kChunk, t.e[i].n - at);
-    if (is_fp32(t, i))
-      chunk_scale(static_cast<const float*>(t.e[i].src) + at, static_cast<float*>(t.e[i].dst) + at, n, k);
-    else
-      chunk_scale(static_cast<const uint16_t*>(t.e[i].src) + at, static_cast<uint16_t*>(t.e[i].dst) + at, n, k);
+  if (threadIdx.x == 0) {
+    *norm_out = (float)norm;
+    *factor = norm > max_norm && norm < __builtin_inf() ? (float)(max_norm / norm) : 1.0f;
   }
+}
+
+__global__ __launch_bounds__(kThreads) void scale_kernel(Table t, const float* __restrict__ factor) {
+  // from the back: what the sum read last may still be cached
+  const int64_t c = t.chunks - 1 - blockIdx.x;
+  const int i = tensor_of(t, c);
+  const float k = *factor;
+  if (k == 1.0f && t.e[i].src == t.e[i].dst) return;  // nothing to change in place
+  const int64_t chunk = chunk_of(is_fp32(t, i)), at = (c - t.e[i].first) * chunk;
+  const int n = (int)min(chunk, t.e[i].n - at);
+  if (is_fp32(t, i))
+    chunk_scale(static_cast<const float*>(t.e[i].src) + at, static_cast<float*>(t.e[i].dst) + at, n, k);
+  else
+    chunk_scale(static_cast<const uint16_t*>(t.e[i].src) + at, static_cast<uint16_t*>(t.e[i].dst) + at, n, k);
 }
 
 // Table of the tensors from `from` on; empty tensors take no place.
@@ -131,14 +223,13 @@ int32_t fill(Table& t, const moeq_grad* g, int32_t count, int32_t from) {
     e.dst = g[i].dst;
     e.n = g[i].numel;
     e.first = t.chunks;
-    t.chunks += (e.n + kChunk - 1) / kChunk;
+    const int64_t chunk = chunk_of(g[i].dtype == MOEQ_DTYPE_FP32);
+    t.chunks += (e.n + chunk - 1) / chunk;
     if (g[i].dtype == MOEQ_DTYPE_FP32) t.fp32[t.count >> 5] |= 1u << (t.count & 31);
     ++t.count;
   }
   return i;
 }
-
-int grid_of(const Table& t) { return (int)(t.chunks < kMaxGrid ? t.chunks : kMaxGrid); }
 
 }  // namespace
 
@@ -147,25 +238,26 @@ int64_t clip_partials(int32_t count) { return ((int64_t)count + kTable - 1) / kT
 hipError_t launch_clip(const moeq_grad* g, int32_t count, double max_norm, float* norm, double* partial, hipStream_t s) {
   Table t;
   int32_t partials = 0;
+  float* factor = reinterpret_cast<float*>(partial);  // (of the sum over the partials, kept in front of them)
+  partial += kClipHead;
   for (int32_t i = 0; i < count;) {
     i = fill(t, g, count, i);
     if (t.count == 0) break;
-    const int grid = grid_of(t);
+    const int grid = (int)(t.chunks < kMaxGrid ? t.chunks : kMaxGrid);
     sum_kernel<<<grid, kThreads, 0, s>>>(t, partial + partials);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     partials += grid;
   }
-  int32_t i = 0;
-  do {  // (no tensor at all, or only empty ones: one workgroup writes the norm, 0)
+  norm_kernel<<<1, kThreads, 0, s>>>(partial, partials, max_norm, norm, factor);
+  hipError_t e = hipGetLastError();
+  for (int32_t i = 0; i < count && e == hipSuccess;) {
     i = fill(t, g, count, i);
-    const int grid = t.count ? grid_of(t) : 1;
-    scale_kernel<<<grid, kThreads, 0, s>>>(t, partial, partials, max_norm, norm);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    norm = nullptr;  // written by the first launch
-  } while (i < count && t.count);
-  return hipSuccess;
+    if (t.count == 0) break;
+    scale_kernel<<<(unsigned)t.chunks, kThreads, 0, s>>>(t, factor);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace moeq

@@ -29,8 +29,9 @@ hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s);
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s);
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s);
 
-// Gradient clipping.  partial: clip_partials(count) fp64.
-constexpr int kClipPartials = 1024;  // partial sums per launch, at most
+// Gradient clipping.  partial: kClipHead + clip_partials(count) fp64.
+constexpr int kClipPartials = 768;  // partial sums per launch, at most
+constexpr int kClipHead = 2;        // room for the factor, in front of the partial sums
 int64_t clip_partials(int32_t count);
 hipError_t launch_clip(const moeq_grad* g, int32_t count, double max_norm, float* norm, double* partial, hipStream_t s);
 
