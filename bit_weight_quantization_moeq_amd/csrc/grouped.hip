@@ -35,6 +35,8 @@
 //
 // offsets are data on the device: they are clamped to [0, M] and no tile
 // leaves the arrays whatever they hold.
+#include <algorithm>
+
 #include "grouped.h"
 
 namespace moeq {
@@ -60,22 +62,41 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
-// Resource of `bytes` bytes at p, with every value in scalar registers.
-__device__ __forceinline__ u32x4 resource(const char* p, int64_t bytes) {
-  const uint64_t a = (uint64_t)p;
-  const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
-                   (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes > 0 ? bytes : 0)), 0x00020000u};
-  return r;
-}
+// s_waitcnt immediate: at most N vector-memory loads outstanding and every LDS
+// access of this wave done (gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt
+// 6:4, lgkmcnt 11:8).
+template <int N>
+constexpr int kWaitLoads = (N & 0xF) | ((N >> 4) << 14) | (0x7 << 4);
 
-// 16 bytes per lane from resource r at byte off into LDS at lds + 16 * lane;
-// zeros past the resource's end.  Inline assembly (with no register output)
-// so that the compiler does not order later LDS reads behind it: the waits
-// before the barriers do.  The DMA reads M0 one wait state after its write.
-__device__ __forceinline__ void dma16(u32x4 r, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
-               : "memory", "m0");
+// Resource of `bytes` bytes at p (none if negative).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const char* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, bytes > 0 ? (int)bytes : 0, 0x00020000);
+}
+// 16 bytes per lane at byte off, zeros past the resource's end: into registers,
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+// or into LDS at lds + 16 * lane.  The address is a bare number: with a
+// pointer to the array the compiler would make later LDS reads wait for all
+// copies in flight; the waits before the barriers order them instead.  For
+// ds_read_b64_tr_b16 the compiler waits all the same, so the bf16 kernels
+// copy through inline assembly (with no register output), which it does not
+// look into; the MXFP4 kernel has loads of its own between the copies, whose
+// waits it counts right only if it sees both.  The DMA reads M0 one wait state
+// after its write.
+template <bool kSeen>
+__device__ __forceinline__ void dma16(const char* p, int64_t bytes, uint32_t off, uint32_t lds) {
+  if constexpr (kSeen) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer(p, bytes), (__attribute__((address_space(3))) void*)(size_t)lds, 16,
+                                             (int)off, 0, 0, 0);
+  } else {
+    const uint64_t a = (uint64_t)p;
+    const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                     (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes > 0 ? bytes : 0)), 0x00020000u};
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory", "m0");
+  }
 }
 
 // One operand's side of a tile: kC rows (contraction-contiguous, !kT) or
@@ -113,22 +134,20 @@ struct Side {
     chunk16 = 16 * ((lane % kLpr) ^ swz(r));
     voff = (uint32_t)r * (uint32_t)stride + (uint32_t)chunk16;
   }
-  // resource of step ks
-  __device__ __forceinline__ u32x4 step(int ks) const {
-    if (!kT) return resource(base, bytes);
-    const int64_t skip = (int64_t)ks * 64 * stride;
-    const int64_t left = bytes - skip;
-    const int64_t most = (int64_t)64 * stride;
-    return resource(base + skip, left < most ? left : most);
-  }
   // instruction i of step ks into the LDS tile at lds
-  __device__ __forceinline__ void dma(u32x4 r, int ks, int i, int wave, uint32_t lds) const {
+  template <bool kSeen>
+  __device__ __forceinline__ void dma(int ks, int i, int wave, uint32_t lds) const {
     uint32_t off = voff + (uint32_t)(i * kRpi * kNW) * (uint32_t)stride;
-    if (!kT) {
+    const char* p = base;
+    int64_t n = bytes;
+    if constexpr (kT) {
+      p += (int64_t)ks * 64 * stride;
+      n = min(n - (int64_t)ks * 64 * stride, (int64_t)64 * stride);
+    } else {
       off += (uint32_t)ks * kStepBytes;
       off = ks * kStepBytes + chunk16 < kbytes ? off : kPast;
     }
-    dma16(r, off, lds + (uint32_t)(i * kNW + wave) * 1024u);
+    dma16<kSeen>(p, n, off, lds + (uint32_t)(i * kNW + wave) * 1024u);
   }
   // Operand fragment of the 32 rows / columns from c0 on at MFMA step s:
   // lane (l32, h) gets contraction chunk 4 h + s (8 bf16, or one MXFP4 block).
@@ -149,57 +168,71 @@ struct Side {
   }
 };
 
-// Scale bytes of MXFP4 rows: eight per row and step.
+// Scale bytes of an MXFP4 row, eight per step, zeros past its end.  The loads
+// have no branch around them: past the row's last eight bytes those are read
+// and shifted down, and a row that is not there (or shorter than eight
+// blocks, whose only step first() loads) reads zeros.
+__device__ const uint64_t kNoScales = 0;
 struct ScaleRow {
-  const uint8_t* p;  // the row's scales, or nullptr past the tile
-  int32_t n;         // scales per row
+  typedef __attribute__((address_space(1))) const uint8_t* Ptr;   // global, so that no load is a flat one
+  Ptr p;
+  int32_t n, lim;   // scales of the row; the last offset to load from
+  __device__ __forceinline__ void init(const uint8_t* row, int n_) {
+    const bool in = row && n_ >= 8;
+    p = (Ptr)(in ? row : reinterpret_cast<const uint8_t*>(&kNoScales));
+    n = n_;
+    lim = in ? n_ - 8 : 0;
+  }
   __device__ __forceinline__ uint2 load(int ks) const {
-    uint2 v = make_uint2(0u, 0u);
-    if (!p) return v;
-    const int at = 8 * ks;
-    if (at + 8 <= n) {
-      __builtin_memcpy(&v, p + at, 8);
-    } else {
-      uint64_t b = 0;
-      for (int i = 0; at + i < n; ++i) b |= (uint64_t)p[at + i] << (8 * i);
-      v = make_uint2((uint32_t)b, (uint32_t)(b >> 32));
-    }
-    return v;
+    const int at = 8 * ks, half = 4 * min(max(at + 8 - n, 0), 8);
+    typedef uint64_t u64a __attribute__((aligned(1)));
+    uint64_t v = *(__attribute__((address_space(1))) const u64a*)(p + min(at, lim));
+    v = (v >> half) >> half;
+    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+  }
+  __device__ __forceinline__ static uint2 first(const uint8_t* row, int n) {
+    uint64_t v = 0;
+    if (row)
+      for (int i = 0; i < n && i < 8; ++i) v |= (uint64_t)row[i] << (8 * i);
+    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
   }
 };
 
 // Shape of a tile: kNWN x kNWM waves, each kTN blocks of 32 columns by kTM
-// blocks of 32 rows.
-template <bool kMX, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM>
+// blocks of 32 rows; kBufs LDS buffers, copies kBufs - 1 steps ahead.
+template <bool kMX, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 struct Tile {
   static constexpr int kNW = kNWN * kNWM;
   static constexpr int kCols = 32 * kTN * kNWN, kRows = 32 * kTM * kNWM;
   using A = Side<kAT, kCols, kNW>;
   using B = Side<kBT, kRows, kNW>;
   static constexpr int kBuf = A::kBytes + B::kBytes;
-  static constexpr int kScaleBuf = kMX ? 8 * (kCols + kRows) : 0;
+  static constexpr int kScaleBuf = kMX ? 8 * 64 * kNW : 0;   // every thread stores a row's
+  static_assert(!kMX || kCols + kRows <= 64 * kNW, "a thread per scale row");
   static constexpr int kInstr = A::kInstr + B::kInstr;
+  static constexpr int kAhead = kBufs - 1;
+  static constexpr int kLds = kBufs * (kBuf + kScaleBuf);
 
   // acc[n][m]: 32 columns x 32 rows each
-  __device__ __forceinline__ static void run(char* smem, const A& a, const B& b, ScaleRow sr, int nks,
+  __device__ __forceinline__ static void run(char* smem, const A& a, const B& b, const uint8_t* scales, int nscale, int nks,
                                              f32x16 (&acc)[kTN][kTM]) {
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
     asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
-    char* sc = smem + 2 * kBuf;     // MX: scales, kCols then kRows rows of 8 B, two buffers
+    char* sc = smem + kBufs * kBuf;  // MX: scales, kCols then kRows rows of 8 B per buffer
 
-    u32x4 ra, rb;
+    // step ks's copies, instruction i, into buffer buf
     auto dma = [&](int ks, int buf, int i) {
       const uint32_t l = lds0 + (uint32_t)buf * kBuf;
       if (i < A::kInstr)
-        a.dma(ra, ks, i, wave, l);
+        a.template dma<kMX>(ks, i, wave, l);
       else
-        b.dma(rb, ks, i - A::kInstr, wave, l + A::kBytes);
+        b.template dma<kMX>(ks, i - A::kInstr, wave, l + A::kBytes);
     };
     auto scale_store = [&](int buf, uint2 v) {
-      if (t < kCols + kRows) *reinterpret_cast<uint2*>(sc + buf * kScaleBuf + 8 * t) = v;
+      *reinterpret_cast<uint2*>(sc + buf * kScaleBuf + 8 * t) = v;
     };
     auto frags = [&](const char* buf, int s, u32x4 (&fa)[kTN], u32x4 (&fb)[kTM]) {
 #pragma unroll
@@ -207,40 +240,48 @@ struct Tile {
 #pragma unroll
       for (int m = 0; m < kTM; ++m) fb[m] = B::frag(buf + A::kBytes, 32 * (kTM * wm + m), s, lane);
     };
+    // End of a step: the next step's copies have landed (loads complete in
+    // order, and only the newest kAhead - 1 steps' may be in flight) and every
+    // LDS access of this step is done before any wave goes on.
+    auto step_end = [&] {
+      __builtin_amdgcn_s_waitcnt(kWaitLoads<(kAhead - 1) * kInstr>);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    };
 
-    ra = a.step(0);
-    rb = b.step(0);
+    ScaleRow sr;
+    if constexpr (kMX) sr.init(scales, nscale);
 #pragma unroll
-    for (int i = 0; i < kInstr; ++i) dma(0, 0, i);
-    if constexpr (kMX) scale_store(0, sr.load(0));
-    __builtin_amdgcn_s_waitcnt(0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    for (int p = 0; p < kAhead; ++p) {
+      if constexpr (kMX) scale_store(p, p == 0 && nscale < 8 ? ScaleRow::first(scales, nscale) : sr.load(p));
+#pragma unroll
+      for (int i = 0; i < kInstr; ++i) dma(p, p, i);
+    }
+    step_end();
 
+    int buf = 0, into = kAhead;   // buffers of this step and of the step copied
     for (int ks = 0; ks < nks; ++ks) {
-      const int buf = ks & 1;
       const char* tile = smem + buf * kBuf;
       uint2 sv = make_uint2(0u, 0u);
       uint32_t sa[kTN], sb[kTM];
       if constexpr (kMX) {
-        if (ks + 1 < nks) sv = sr.load(ks + 1);
+        sv = sr.load(ks + kAhead);
         const char* s0 = sc + buf * kScaleBuf + 8 * (lane & 31) + 4 * (lane >> 5);
 #pragma unroll
         for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
 #pragma unroll
         for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
       }
-      ra = a.step(ks + 1);  // (past the last step everything is out of range)
-      rb = b.step(ks + 1);
       u32x4 fa[2][kTN], fb[2][kTM];
       frags(tile, 0, fa[0], fb[0]);
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
         if (s + 1 < kSub) frags(tile, s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
-        // the next step's copies, in the first three quarters of this one
+        // a later step's copies, in the first three quarters of this one (past
+        // the last step everything is out of range)
 #pragma unroll
         for (int i = s * kInstr / (kSub - 1); i < (s + 1) * kInstr / (kSub - 1) && i < kInstr; ++i)
-          dma(ks + 1, buf ^ 1, i);
+          dma(ks + kAhead, into, i);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < kTN; ++n)
@@ -267,13 +308,13 @@ struct Tile {
           }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (kMX) scale_store(buf ^ 1, sv);
-      // Every copy of the next step has landed and every LDS access of this
-      // one is done before any wave goes on.
-      __builtin_amdgcn_s_waitcnt(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      if constexpr (kMX) scale_store(into, sv);
+      step_end();
+      buf = buf + 1 == kBufs ? 0 : buf + 1;
+      into = into + 1 == kBufs ? 0 : into + 1;
     }
+    __builtin_amdgcn_s_waitcnt(0);   // copies of steps past the end
+    __syncthreads();
   }
 
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
@@ -386,9 +427,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, 
 
 // forward (kAT = false, kMX or not) and grad_input (kAT = true).
 //   x [M][kc], w [E][..], out [M][nout]: kc contraction length, nout columns.
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM>
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int e, int row0, int nrows, int c0) {
-  using T = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM>;
+  using T = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
   typename T::A a;
@@ -402,12 +443,13 @@ __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int 
     a.init(w + ((int64_t)e * g.nout + c0) * kbytes, (int64_t)ncols * kbytes, kbytes, kbytes, wave, lane);
   }
   b.init(static_cast<const char*>(g.x) + (int64_t)row0 * kbytes, (int64_t)nrows * kbytes, kbytes, kbytes, wave, lane);
-  ScaleRow sr = {nullptr, g.kc / 32};
+  const int nscale = g.kc / 32;
+  const uint8_t* scales = nullptr;   // of this thread's row of the tile: the columns, then the rows
   if constexpr (kMX) {
     if (t < T::kCols) {
-      if (t < ncols) sr.p = g.w_scales + ((int64_t)e * g.nout + c0 + t) * sr.n;
+      if (t < ncols) scales = g.w_scales + ((int64_t)e * g.nout + c0 + t) * nscale;
     } else if (t - T::kCols < nrows) {
-      sr.p = g.x_scales + (int64_t)(row0 + t - T::kCols) * sr.n;
+      scales = g.x_scales + (int64_t)(row0 + t - T::kCols) * nscale;
     }
   }
   f32x16 acc[kTN][kTM];
@@ -415,34 +457,33 @@ __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int 
   for (int n = 0; n < kTN; ++n)
 #pragma unroll
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
-  T::run(smem, a, b, sr, (kbytes + kStepBytes - 1) / kStepBytes, acc);
+  T::run(smem, a, b, scales, nscale, (kbytes + kStepBytes - 1) / kStepBytes, acc);
   T::store(smem, acc, static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.nout + c0, g.nout, nrows, ncols);
 }
 
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN>
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 __global__ __launch_bounds__(64 * kNWN * kNWM, 2) void rows_kernel(GroupedArgs g) {
-  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, 4>;
-  __shared__ __attribute__((aligned(16))) char smem[imax(2 * Big::kBuf + 2 * Big::kScaleBuf, Big::out_bytes(2))];
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
+  __shared__ __attribute__((aligned(16))) char smem[imax(Big::kLds, Big::out_bytes(2))];
   int e, row0, nrows, ct;
   if (!find_tile(g.offsets, g.E, g.M, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
   const int c0 = ct * Big::kCols;
   // blocks of 32 rows per wave: as few as the tile's rows need
-  if (nrows > 3 * 32 * kNWM)
-    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 4>(smem, g, e, row0, nrows, c0);
-  else if (nrows > 2 * 32 * kNWM)
-    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 3>(smem, g, e, row0, nrows, c0);
-  else if (nrows > 32 * kNWM)
-    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 2>(smem, g, e, row0, nrows, c0);
-  else
-    rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1>(smem, g, e, row0, nrows, c0);
+  if constexpr (kTM > 3)
+    if (nrows > 3 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 4, kBufs>(smem, g, e, row0, nrows, c0);
+  if constexpr (kTM > 2)
+    if (nrows > 2 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 3, kBufs>(smem, g, e, row0, nrows, c0);
+  if constexpr (kTM > 1)
+    if (nrows > 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 2, kBufs>(smem, g, e, row0, nrows, c0);
+  rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1, kBufs>(smem, g, e, row0, nrows, c0);
 }
 
 // grad_weight: tile of dw[e] [N][K]: rows n (dy columns, B), columns k (x
 // columns, A), contraction over the expert's rows.
-template <typename Out, int kNWN, int kNWM, int kTN, int kTM>
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 __global__ __launch_bounds__(64 * kNWN * kNWM, 2) void weight_kernel(GroupedArgs g) {
-  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM>;
-  __shared__ __attribute__((aligned(16))) char smem[imax(2 * T::kBuf, T::out_bytes(sizeof(Out)))];
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufs>;
+  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(sizeof(Out)))];
   const int N = g.nout, K = g.kc;
   const int nk = (K + T::kCols - 1) / T::kCols, nn = (N + T::kRows - 1) / T::kRows;
   const int total = g.E * nn * nk, per = (total + kXcds - 1) / kXcds;
@@ -466,42 +507,213 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, 2) void weight_kernel(GroupedArgs
   for (int n = 0; n < kTN; ++n)
 #pragma unroll
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
-  T::run(smem, a, b, ScaleRow{nullptr, 0}, (cnt + 63) / 64, acc);
+  T::run(smem, a, b, nullptr, 0, (cnt + 63) / 64, acc);
   T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)e * N + n0) * K + k0, K, min(T::kRows, N - n0),
            min(T::kCols, K - k0));
 }
 
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN>
-hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
-  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, 4>;
-  const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
-  const int64_t tiles = (int64_t)g.M / Big::kRows + (g.E < g.M ? g.E : g.M);
-  const int64_t grid = (tiles * ncol + kXcds - 1) / kXcds * kXcds;
-  rows_kernel<kMX, kAT, kNWN, kNWM, kTN><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+// ---------------------------------------------------------------------------
+// Few rows per expert (decode): the product streams the weights once and the
+// matrix cores have time to spare, so a workgroup takes at most 16 rows of an
+// expert and 16 kTN columns, and its waves split the contraction.  A wave
+// reads units of 256 B of its weight rows straight into MFMA operands
+// (16x16x32 bf16 / 16x16x128 MXFP4), one unit ahead, lane group g = lane / 16
+// holding chunk 4 j + g of the unit for MFMA j, so that 64 consecutive bytes
+// of 16 rows are read at a time.  The waves' sums are added in wave order
+// through LDS.
+// ---------------------------------------------------------------------------
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kUnitBytes = 256;
+constexpr int kFewRowsGroups = 2048;
+
+// Sixteen scale bytes of a row: those of unit u, zeros past the row's end
+// (where the last sixteen of the row are read and shifted down).
+__device__ __forceinline__ u32x4 unit_scales(const uint8_t* p, int n, int u) {
+  uint64_t v[2] = {0, 0};
+  const int at = 16 * u;
+  if (p && at < n) {
+    const int over = at + 16 - n;   // the same for all lanes
+    if (n < 16) {
+      for (int i = 0; i < min(n, 8); ++i) v[0] |= (uint64_t)p[i] << (8 * i);
+      for (int i = 8; i < n; ++i) v[1] |= (uint64_t)p[i] << (8 * (i - 8));
+    } else {
+      __builtin_memcpy(v, p + (over > 0 ? n - 16 : at), 16);
+      if (over >= 8) {
+        v[0] = v[1] >> (8 * (over - 8));
+        v[1] = 0;
+      } else if (over > 0) {
+        v[0] = v[0] >> (8 * over) | v[1] << (64 - 8 * over);
+        v[1] >>= 8 * over;
+      }
+    }
+  }
+  return u32x4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)};
+}
+
+template <bool kMX, int kTN, int kNW>
+__global__ __launch_bounds__(64 * kNW) void few_rows_kernel(GroupedArgs g, int span) {
+  constexpr int kCols = 16 * kTN;
+  __shared__ __attribute__((aligned(16))) f32x4 part[2][kNW][kTN][64];
+  const int ntile = (g.nout + kCols - 1) / kCols;
+  int e, row0, nrows, ct;
+  if (!find_tile(g.offsets, g.E, g.M, 16, (ntile + span - 1) / span, e, row0, nrows, ct)) return;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int l16 = lane & 15, grp = lane >> 4;
+  const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
+  const int tile0 = ct * span, tiles = min(span, ntile - tile0);
+  const __amdgpu_buffer_rsrc_t rx = buffer(static_cast<const char*>(g.x) + (int64_t)row0 * kbytes, (int64_t)nrows * kbytes);
+  const char* wbase = static_cast<const char*>(g.w) + (int64_t)e * g.nout * kbytes;
+  const int nscale = g.kc / 32;
+  const uint8_t* xs = nullptr;
+  if constexpr (kMX)
+    if (l16 < nrows) xs = g.x_scales + (int64_t)(row0 + l16) * nscale;
+
+  struct Unit {
+    u32x4 w[kTN][4], x[4], sw[kTN], sx;
+  };
+  // step i of this wave: its unit i % steps (of units wave, wave + kNW, ...) of
+  // the workgroup's column tile i / steps; what is out of range loads zeros
+  const int units = (kbytes + kUnitBytes - 1) / kUnitBytes, steps = (units + kNW - 1) / kNW;
+  auto load = [&](Unit& v, int tile, int step) {
+    const int u = step * kNW + wave, c0 = (tile0 + tile) * kCols, ncols = min(kCols, g.nout - c0);
+    const __amdgpu_buffer_rsrc_t rw = buffer(wbase + (int64_t)c0 * kbytes, (int64_t)ncols * kbytes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = u * kUnitBytes + 64 * j + 16 * grp;
+      const bool in = at < kbytes;
+#pragma unroll
+      for (int n = 0; n < kTN; ++n)
+        v.w[n][j] = buffer_load16(rw, in ? (uint32_t)(16 * n + l16) * (uint32_t)kbytes + (uint32_t)at : kPast);
+      v.x[j] = buffer_load16(rx, in ? (uint32_t)l16 * (uint32_t)kbytes + (uint32_t)at : kPast);
+    }
+    if constexpr (kMX) {
+      v.sx = unit_scales(xs, nscale, u);
+      const uint8_t* ws = g.w_scales + ((int64_t)e * g.nout + c0 + l16) * nscale;
+#pragma unroll
+      for (int n = 0; n < kTN; ++n)
+        v.sw[n] = unit_scales(16 * n + l16 < ncols ? ws + (int64_t)16 * n * nscale : nullptr, nscale, u);
+    }
+  };
+  f32x4 acc[kTN];
+#pragma unroll
+  for (int n = 0; n < kTN; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Unit& v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int n = 0; n < kTN; ++n) {
+        if constexpr (kMX) {
+          const u32x4 a = v.w[n][j], b = v.x[j];
+          const i32x8 xa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+          const i32x8 xb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+          acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, xb, acc[n], 4, 4, 0, v.sw[n][j] >> (8 * grp), 0,
+                                                                    v.sx[j] >> (8 * grp));
+        } else {
+          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.w[n][j]),
+                                                           __builtin_bit_cast(bf16x8, v.x[j]), acc[n], 0, 0, 0);
+        }
+      }
+  };
+  // The sums of a finished column tile, and its stores.  Two buffers in turn:
+  // a wave is past the barrier of one tile before it writes the next one's.
+  auto finish = [&](int tile) {
+    auto& p = part[tile & 1];
+#pragma unroll
+    for (int n = 0; n < kTN; ++n) {
+      p[wave][n][lane] = acc[n];
+      acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // (an LDS barrier: the next unit's loads stay in flight)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    const int c0 = (tile0 + tile) * kCols;
+    // lane l of block n holds columns 16 n + 4 (l / 16) .. +3 of row l % 16
+    for (int i = t; i < kTN * 64; i += 64 * kNW) {
+      const int n = i >> 6, l = i & 63, c = c0 + 16 * n + 4 * (l >> 4), r = l & 15;
+      f32x4 s = p[0][n][l];
+#pragma unroll
+      for (int v = 1; v < kNW; ++v) {
+        const f32x4 q = p[v][n][l];
+        s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
+      }
+      if (r < nrows && c < g.nout)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + r) * g.nout + c) =
+            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  };
+  Unit va, vb;
+  int tile = 0, step = 0;   // of the unit in use
+  const int total = tiles * steps;
+  auto advance = [&](Unit& cur, Unit& nxt, int i) {
+    const bool last = step + 1 == steps;
+    if (i + 1 < total) load(nxt, last ? tile + 1 : tile, last ? 0 : step + 1);
+    use(cur);
+    if (last) finish(tile);
+    tile += last ? 1 : 0;
+    step = last ? 0 : step + 1;
+  };
+  load(va, 0, 0);
+  for (int i = 0; i < total; i += 2) {
+    advance(va, vb, i);
+    if (i + 1 < total) advance(vb, va, i + 1);
+  }
+}
+
+template <bool kMX, int kTN, int kNW>
+hipError_t launch_few_rows(const GroupedArgs& g, hipStream_t s) {
+  const int64_t ntile = (g.nout + 16 * kTN - 1) / (16 * kTN);
+  const int64_t slots = (int64_t)g.M / 16 + (g.E < g.M ? g.E : g.M);
+  // column tiles a workgroup takes in turn: enough workgroups to fill the
+  // card a few times over, so that its prefetch runs on from tile to tile
+  const int64_t span = std::max<int64_t>(1, std::min<int64_t>(ntile, slots * ntile / kFewRowsGroups));
+  const int64_t grid = (slots * ((ntile + span - 1) / span) + kXcds - 1) / kXcds * kXcds;
+  few_rows_kernel<kMX, kTN, kNW><<<(unsigned)grid, 64 * kNW, 0, s>>>(g, (int)span);
   return hipGetLastError();
 }
 
-template <typename Out, int kNWN, int kNWM, int kTN, int kTM>
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
+  const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
+  const int64_t tiles = (int64_t)g.M / Big::kRows + (g.E < g.M ? g.E : g.M);
+  const int64_t grid = (tiles * ncol + kXcds - 1) / kXcds * kXcds;
+  rows_kernel<kMX, kAT, kNWN, kNWM, kTN, kTM, kBufs><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
-  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM>;
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufs>;
   const int64_t total = (int64_t)g.E * ((g.nout + T::kRows - 1) / T::kRows) * ((g.kc + T::kCols - 1) / T::kCols);
   const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
-  weight_kernel<Out, kNWN, kNWM, kTN, kTM><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  weight_kernel<Out, kNWN, kNWM, kTN, kTM, kBufs><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) { return launch_rows<false, false, 4, 2, 2>(g, s); }
+// Whether the rows are so few that the product streams weights for them.
+bool few_rows(const GroupedArgs& g) { return g.M <= 16 * g.E; }
 
-hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) { return launch_rows<true, false, 4, 2, 2>(g, s); }
+hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) {
+  if (few_rows(g)) return launch_few_rows<false, 1, 4>(g, s);
+  return launch_rows<false, false, 4, 2, 2, 4, 2>(g, s);
+}
+
+hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) {
+  if (few_rows(g)) return launch_few_rows<true, 1, 4>(g, s);
+  return launch_rows<true, false, 4, 2, 2, 4, 2>(g, s);
+}
 
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
-  return launch_rows<false, true, 4, 2, 2>(g, s);
+  return launch_rows<false, true, 4, 2, 2, 4, 2>(g, s);
 }
 
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
-  return fp32 ? launch_weight<float, 4, 2, 2, 4>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4>(g, s);
+  return fp32 ? launch_weight<float, 4, 2, 2, 4, 2>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4, 2>(g, s);
 }
 
 }  // namespace moeq
