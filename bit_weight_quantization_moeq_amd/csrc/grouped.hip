@@ -36,6 +36,7 @@
 // offsets are data on the device: they are clamped to [0, M] and no tile
 // leaves the arrays whatever they hold.
 #include <algorithm>
+#include <type_traits>
 
 #include "grouped.h"
 
@@ -183,35 +184,38 @@ struct ScaleRow {
     n = n_;
     lim = in ? n_ - 8 : 0;
   }
-  __device__ __forceinline__ uint2 load(int ks) const {
-    const int at = 8 * ks, half = 4 * min(max(at + 8 - n, 0), 8);
+  __device__ __forceinline__ uint64_t load(int ks) const {
     typedef uint64_t u64a __attribute__((aligned(1)));
-    uint64_t v = *(__attribute__((address_space(1))) const u64a*)(p + min(at, lim));
-    v = (v >> half) >> half;
-    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+    return *(__attribute__((address_space(1))) const u64a*)(p + min(8 * ks, lim));
   }
-  __device__ __forceinline__ static uint2 first(const uint8_t* row, int n) {
+  // what load(ks) returned, in place
+  __device__ __forceinline__ uint64_t use(uint64_t v, int ks) const {
+    const int half = 4 * min(max(8 * ks + 8 - n, 0), 8);
+    return (v >> half) >> half;
+  }
+  __device__ __forceinline__ static uint64_t first(const uint8_t* row, int n) {
     uint64_t v = 0;
     if (row)
       for (int i = 0; i < n && i < 8; ++i) v |= (uint64_t)row[i] << (8 * i);
-    return make_uint2((uint32_t)v, (uint32_t)(v >> 32));
+    return v;
   }
 };
 
 // Shape of a tile: kNWN x kNWM waves, each kTN blocks of 32 columns by kTM
-// blocks of 32 rows; kBufs LDS buffers, copies kBufs - 1 steps ahead.
-template <bool kMX, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+// blocks of 32 rows; kBufsA and kBufsB LDS buffers of the columns' and of the
+// rows' operand.
+template <bool kMX, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 struct Tile {
   static constexpr int kNW = kNWN * kNWM;
   static constexpr int kCols = 32 * kTN * kNWN, kRows = 32 * kTM * kNWM;
   using A = Side<kAT, kCols, kNW>;
   using B = Side<kBT, kRows, kNW>;
-  static constexpr int kBuf = A::kBytes + B::kBytes;
+  static constexpr int kBytesB = kBufsA * A::kBytes;   // where the rows' buffers start
   static constexpr int kScaleBuf = kMX ? 8 * 64 * kNW : 0;   // every thread stores a row's
   static_assert(!kMX || kCols + kRows <= 64 * kNW, "a thread per scale row");
   static constexpr int kInstr = A::kInstr + B::kInstr;
-  static constexpr int kAhead = kBufs - 1;
-  static constexpr int kLds = kBufs * (kBuf + kScaleBuf);
+  static constexpr int kScales = kBytesB + kBufsB * B::kBytes;   // and the scales'
+  static constexpr int kLds = kScales + 2 * kScaleBuf;
 
   // acc[n][m]: 32 columns x 32 rows each
   __device__ __forceinline__ static void run(char* smem, const A& a, const B& b, const uint8_t* scales, int nscale, int nks,
@@ -221,67 +225,95 @@ struct Tile {
     const int wn = wave % kNWN, wm = wave / kNWN;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
     asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
-    char* sc = smem + kBufs * kBuf;  // MX: scales, kCols then kRows rows of 8 B per buffer
+    char* sc = smem + kScales;   // MX: kCols then kRows rows of 8 B in each of two buffers
 
-    // step ks's copies, instruction i, into buffer buf
-    auto dma = [&](int ks, int buf, int i) {
-      const uint32_t l = lds0 + (uint32_t)buf * kBuf;
-      if (i < A::kInstr)
-        a.template dma<kMX>(ks, i, wave, l);
-      else
-        b.template dma<kMX>(ks, i - A::kInstr, wave, l + A::kBytes);
+    // instruction i of step ks's copies into ring slot `slot`
+    auto dma_a = [&](int ks, int slot, int i) { a.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(slot * A::kBytes)); };
+    auto dma_b = [&](int ks, int slot, int i) {
+      b.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(kBytesB + slot * B::kBytes));
     };
-    auto scale_store = [&](int buf, uint2 v) {
-      *reinterpret_cast<uint2*>(sc + buf * kScaleBuf + 8 * t) = v;
+    auto scale_store = [&](int buf, uint64_t v) {
+      *reinterpret_cast<uint64_t*>(sc + buf * kScaleBuf + 8 * t) = v;
     };
-    auto frags = [&](const char* buf, int s, u32x4 (&fa)[kTN], u32x4 (&fb)[kTM]) {
-#pragma unroll
-      for (int n = 0; n < kTN; ++n) fa[n] = A::frag(buf, 32 * (kTN * wn + n), s, lane);
-#pragma unroll
-      for (int m = 0; m < kTM; ++m) fb[m] = B::frag(buf + A::kBytes, 32 * (kTM * wm + m), s, lane);
-    };
-    // End of a step: the next step's copies have landed (loads complete in
-    // order, and only the newest kAhead - 1 steps' may be in flight) and every
-    // LDS access of this step is done before any wave goes on.
-    auto step_end = [&] {
-      __builtin_amdgcn_s_waitcnt(kWaitLoads<(kAhead - 1) * kInstr>);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    };
-
-    ScaleRow sr;
-    if constexpr (kMX) sr.init(scales, nscale);
-#pragma unroll
-    for (int p = 0; p < kAhead; ++p) {
-      if constexpr (kMX) scale_store(p, p == 0 && nscale < 8 ? ScaleRow::first(scales, nscale) : sr.load(p));
-#pragma unroll
-      for (int i = 0; i < kInstr; ++i) dma(p, p, i);
-    }
-    step_end();
-
-    int buf = 0, into = kAhead;   // buffers of this step and of the step copied
-    for (int ks = 0; ks < nks; ++ks) {
-      const char* tile = smem + buf * kBuf;
-      uint2 sv = make_uint2(0u, 0u);
-      uint32_t sa[kTN], sb[kTM];
-      if constexpr (kMX) {
-        sv = sr.load(ks + kAhead);
-        const char* s0 = sc + buf * kScaleBuf + 8 * (lane & 31) + 4 * (lane >> 5);
-#pragma unroll
-        for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
-#pragma unroll
-        for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
+    // the MFMA order is column block by column block: operand j of kOps is
+    // the j-th that it needs (a 0, the b's, the other a's)
+    constexpr int kOps = kTN + kTM, kMfmas = kTN * kTM;
+    auto frag = [&](const char* ta, const char* tb, int s, int j, u32x4 (&fa)[kTN], u32x4 (&fb)[kTM]) {
+      if (j >= 1 && j <= kTM) {
+        fb[j - 1] = B::frag(tb, 32 * (kTM * wm + j - 1), s, lane);
+      } else {
+        const int n = j == 0 ? 0 : j - kTM;
+        fa[n] = A::frag(ta, 32 * (kTN * wn + n), s, lane);
       }
-      u32x4 fa[2][kTN], fb[2][kTM];
-      frags(tile, 0, fa[0], fb[0]);
+    };
+    auto load_scales = [&](int buf, uint32_t (&sa)[kTN], uint32_t (&sb)[kTM]) {
+      const char* s0 = sc + buf * kScaleBuf + 8 * (lane & 31) + 4 * (lane >> 5);
+#pragma unroll
+      for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
+#pragma unroll
+      for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
+    };
+    // The step loop.  The barrier stands before the last MFMA step: by then
+    // every wave holds that step's operands in registers, so that the LDS
+    // buffer is free for a later step's copies, and the next step's first
+    // operands are read during the last MFMAs, so that the matrix cores need
+    // not wait at the turn of a step.  In step ks the columns' copies of step
+    // ks + kBufsA - 1 are spread over the MFMAs before the barrier and the
+    // rows' of step ks + kBufsB over those behind it, one at a time, as are
+    // the operand reads: issued together, the copies hold the wave up at the
+    // memory pipeline.  Loads complete in order, so the barrier's wait can
+    // leave in flight whatever was issued after the next step's copies.
+    constexpr int kInFlight = (kBufsA - 2) * A::kInstr + (kBufsB - 2) * B::kInstr;
+    ScaleRow sr;
+    uint64_t sv = 0;   // scales on their way to LDS: those of step ks + 1
+    uint32_t sa[kTN], sb[kTM];
+    if constexpr (kMX) {
+      sr.init(scales, nscale);
+      scale_store(0, nscale < 8 ? ScaleRow::first(scales, nscale) : sr.use(sr.load(0), 0));
+    }
+    auto fill_a = [&](int p) {
+#pragma unroll
+      for (int i = 0; i < A::kInstr; ++i) dma_a(p, p, i);
+    };
+    auto fill_b = [&](int p) {
+#pragma unroll
+      for (int i = 0; i < B::kInstr; ++i) dma_b(p, p, i);
+    };
+    // in the order of the loop
+#pragma unroll
+    for (int p = 0; p < kBufsA || p < kBufsB; ++p) {
+      if (kBufsA > kBufsB && p < kBufsA - 1) fill_a(p);
+      if (p < kBufsB) fill_b(p);
+      if (kBufsA <= kBufsB && p < kBufsA - 1) fill_a(p);
+    }
+    if constexpr (kMX) sv = sr.load(1);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads<kInFlight + B::kInstr>);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    u32x4 fa[2][kTN], fb[2][kTM];
+#pragma unroll
+    for (int j = 0; j < kOps; ++j) frag(smem, smem + kBytesB, 0, j, fa[0], fb[0]);
+    if constexpr (kMX) load_scales(0, sa, sb);
+
+    int sa0 = 0, sb0 = 0;   // this step's ring slots
+    for (int ks = 0; ks < nks; ++ks) {
+      const int sa1 = sa0 + 1 == kBufsA ? 0 : sa0 + 1, sb1 = sb0 + 1 == kBufsB ? 0 : sb0 + 1;
+      const int sap = sa0 == 0 ? kBufsA - 1 : sa0 - 1;
+      uint32_t na[kTN], nb[kTM];
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
-        if (s + 1 < kSub) frags(tile, s + 1, fa[(s + 1) & 1], fb[(s + 1) & 1]);
-        // a later step's copies, in the first three quarters of this one (past
-        // the last step everything is out of range)
-#pragma unroll
-        for (int i = s * kInstr / (kSub - 1); i < (s + 1) * kInstr / (kSub - 1) && i < kInstr; ++i)
-          dma(ks + kAhead, into, i);
+        if (s + 1 == kSub) {
+          if constexpr (kMX) scale_store((ks + 1) & 1, sr.use(sv, ks + 1));
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<kInFlight>);
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+          if constexpr (kMX) {
+            load_scales((ks + 1) & 1, na, nb);
+            sv = sr.load(ks + 2);
+          }
+        }
+        const char* ta = smem + (s + 1 < kSub ? sa0 : sa1) * A::kBytes;
+        const char* tb = smem + kBytesB + (s + 1 < kSub ? sb0 : sb1) * B::kBytes;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < kTN; ++n)
@@ -305,13 +337,32 @@ struct Tile {
                                                                   __builtin_bit_cast(bf16x8, fb[s & 1][m]),
                                                                   acc[n][m], 0, 0, 0);
             }
+            const int i = n * kTM + m;
+#pragma unroll
+            for (int j = i * kOps / kMfmas; j < (i + 1) * kOps / kMfmas; ++j)
+              frag(ta, tb, (s + 1) % kSub, j, fa[(s + 1) & 1], fb[(s + 1) & 1]);
+            // (past the last step everything is out of range)
+            if (s + 1 < kSub) {
+              constexpr int kSlots = (kSub - 1) * kMfmas;
+#pragma unroll
+              for (int d = 0; d < A::kInstr; ++d)
+                if (s * kMfmas + i == d * kSlots / A::kInstr) dma_a(ks + kBufsA - 1, sap, d);
+            } else {
+#pragma unroll
+              for (int d = 0; d < B::kInstr; ++d)
+                if (i == d * kMfmas / B::kInstr) dma_b(ks + kBufsB, sb0, d);
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
-        __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (kMX) scale_store(into, sv);
-      step_end();
-      buf = buf + 1 == kBufs ? 0 : buf + 1;
-      into = into + 1 == kBufs ? 0 : into + 1;
+      if constexpr (kMX) {
+#pragma unroll
+        for (int n = 0; n < kTN; ++n) sa[n] = na[n];
+#pragma unroll
+        for (int m = 0; m < kTM; ++m) sb[m] = nb[m];
+      }
+      sa0 = sa1;
+      sb0 = sb1;
     }
     __builtin_amdgcn_s_waitcnt(0);   // copies of steps past the end
     __syncthreads();
@@ -427,9 +478,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, 
 
 // forward (kAT = false, kMX or not) and grad_input (kAT = true).
 //   x [M][kc], w [E][..], out [M][nout]: kc contraction length, nout columns.
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int e, int row0, int nrows, int c0) {
-  using T = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
+  using T = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
   typename T::A a;
@@ -461,28 +512,28 @@ __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int 
   T::store(smem, acc, static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.nout + c0, g.nout, nrows, ncols);
 }
 
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
-__global__ __launch_bounds__(64 * kNWN * kNWM, 2) void rows_kernel(GroupedArgs g) {
-  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void rows_kernel(GroupedArgs g) {
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[imax(Big::kLds, Big::out_bytes(2))];
   int e, row0, nrows, ct;
   if (!find_tile(g.offsets, g.E, g.M, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
   const int c0 = ct * Big::kCols;
   // blocks of 32 rows per wave: as few as the tile's rows need
   if constexpr (kTM > 3)
-    if (nrows > 3 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 4, kBufs>(smem, g, e, row0, nrows, c0);
+    if (nrows > 3 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 4, kBufsA, kBufsB>(smem, g, e, row0, nrows, c0);
   if constexpr (kTM > 2)
-    if (nrows > 2 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 3, kBufs>(smem, g, e, row0, nrows, c0);
+    if (nrows > 2 * 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 3, kBufsA, kBufsB>(smem, g, e, row0, nrows, c0);
   if constexpr (kTM > 1)
-    if (nrows > 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 2, kBufs>(smem, g, e, row0, nrows, c0);
-  rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1, kBufs>(smem, g, e, row0, nrows, c0);
+    if (nrows > 32 * kNWM) return rows_tile<kMX, kAT, kNWN, kNWM, kTN, 2, kBufsA, kBufsB>(smem, g, e, row0, nrows, c0);
+  rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1, kBufsA, kBufsB>(smem, g, e, row0, nrows, c0);
 }
 
 // grad_weight: tile of dw[e] [N][K]: rows n (dy columns, B), columns k (x
 // columns, A), contraction over the expert's rows.
-template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
-__global__ __launch_bounds__(64 * kNWN * kNWM, 2) void weight_kernel(GroupedArgs g) {
-  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufs>;
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void weight_kernel(GroupedArgs g) {
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(sizeof(Out)))];
   const int N = g.nout, K = g.kc;
   const int nk = (K + T::kCols - 1) / T::kCols, nn = (N + T::kRows - 1) / T::kRows;
@@ -674,22 +725,22 @@ hipError_t launch_few_rows(const GroupedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
-  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufs>;
+  using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
   const int64_t tiles = (int64_t)g.M / Big::kRows + (g.E < g.M ? g.E : g.M);
   const int64_t grid = (tiles * ncol + kXcds - 1) / kXcds * kXcds;
-  rows_kernel<kMX, kAT, kNWN, kNWM, kTN, kTM, kBufs><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  rows_kernel<kMX, kAT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
   return hipGetLastError();
 }
 
-template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
-  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufs>;
+  using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   const int64_t total = (int64_t)g.E * ((g.nout + T::kRows - 1) / T::kRows) * ((g.kc + T::kCols - 1) / T::kCols);
   const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
-  weight_kernel<Out, kNWN, kNWM, kTN, kTM, kBufs><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  weight_kernel<Out, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -700,20 +751,20 @@ bool few_rows(const GroupedArgs& g) { return g.M <= 16 * g.E; }
 
 hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) {
   if (few_rows(g)) return launch_few_rows<false, 1, 4>(g, s);
-  return launch_rows<false, false, 4, 2, 2, 4, 2>(g, s);
+  return launch_rows<false, false, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
 hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) {
   if (few_rows(g)) return launch_few_rows<true, 1, 4>(g, s);
-  return launch_rows<true, false, 4, 2, 2, 4, 2>(g, s);
+  return launch_rows<true, false, 4, 2, 2, 4, 2, 2>(g, s);
 }
 
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
-  return launch_rows<false, true, 4, 2, 2, 4, 2>(g, s);
+  return launch_rows<false, true, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
-  return fp32 ? launch_weight<float, 4, 2, 2, 4, 2>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4, 2>(g, s);
+  return fp32 ? launch_weight<float, 4, 2, 2, 4, 3, 2>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
 }  // namespace moeq
