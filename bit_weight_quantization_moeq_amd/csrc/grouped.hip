@@ -370,7 +370,9 @@ struct Tile {
 
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
   // out, ld elements a row, staged through LDS so that the stores write whole
-  // rows (from the accumulator layout one instruction would touch 32 rows).
+  // rows (from the accumulator layout one instruction would touch 32 rows),
+  // past the caches, which hold the operands (fp32 grad_weight of E = 64,
+  // N = K = 2048: 409 -> 349 us).
   // Fp32 tiles go by the rows of one row of waves at a time.
   template <typename T>
   __device__ __forceinline__ static void store(char* smem, const f32x16 (&acc)[kTN][kTM], T* out, int64_t ld, int nrows,
@@ -408,8 +410,8 @@ struct Tile {
       for (int c = t; c < kPassRows * kChunks; c += 64 * kNW) {
         const int r = c / kChunks, k = c % kChunks;
         if (first + r < nrows && kPer * k < ncols)
-          *reinterpret_cast<uint4*>(out + (int64_t)(first + r) * ld + kPer * k) =
-              *reinterpret_cast<const uint4*>(smem + r * kOutPitch + 16 * k);
+          __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(smem + r * kOutPitch + 16 * k),
+                                      reinterpret_cast<u32x4*>(out + (int64_t)(first + r) * ld + kPer * k));
       }
     }
   }
@@ -422,6 +424,20 @@ constexpr int imax(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int M, int& lo, int& n) {
   lo = min(max(offsets[e], 0), M);
   n = max(min(offsets[e + 1], M) - lo, 0);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int add_dpp(int v) {
+  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+// Inclusive prefix sum over the wave, in six DPP additions.
+__device__ __forceinline__ int wave_scan(int v) {
+  v = add_dpp<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8 within rows of 16 lanes
+  v = add_dpp<0x112, 0xF>(v);
+  v = add_dpp<0x114, 0xF>(v);
+  v = add_dpp<0x118, 0xF>(v);
+  v = add_dpp<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+  return add_dpp<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
 // Work item of this workgroup among the (expert, row tile, column tile)
@@ -439,22 +455,15 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, 
     return (n + max_rows - 1) / max_rows;
   };
   int lo, n, total = 0;
-  for (int i = 0; i < E; i += 64) total += tiles(i + lane, lo, n);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o, 64);
-  total = __builtin_amdgcn_readfirstlane(total) * ncol;
+  for (int i = 0; i < E; i += 64) total += __builtin_amdgcn_readlane(wave_scan(tiles(i + lane, lo, n)), 63);
+  total *= ncol;
   const int per = (total + kXcds - 1) / kXcds;
   const int slot = blockIdx.x / kXcds, w = (blockIdx.x % kXcds) * per + slot;
   if (slot >= per || w >= total) return false;
   int before = 0;
   for (int i = 0; i < E; i += 64) {
     const int nt = tiles(i + lane, lo, n);
-    int incl = nt;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
+    const int incl = wave_scan(nt);
     const int first = before + incl - nt;
     const uint64_t hit = __ballot(w >= first * ncol && w < (first + nt) * ncol);
     if (hit) {
@@ -744,27 +753,47 @@ hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+
+// Whether the product does little more than stream one operand past the other:
+// few rows per expert (the weights), or few output columns (the rows).
+bool streams(const GroupedArgs& g) { return g.M <= 16 * g.E || g.nout <= 32; }
+
+// Whether tiles of 256 x 256 would leave compute units without work; those of
+// half the columns then do better (and have room for a third buffer).
+bool few_tiles(const GroupedArgs& g) {
+  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
+  return rows * ((g.nout + 255) / 256) <= 256;
+}
+
+template <bool kMX>
+hipError_t launch_forward(const GroupedArgs& g, hipStream_t s) {
+  if (streams(g)) return launch_few_rows<kMX, 1, 4>(g, s);
+  if (few_tiles(g)) return launch_rows<kMX, false, 4, 2, 1, 4, 3, 3>(g, s);
+  // (three buffers of the columns' operand leave no room for the scales)
+  return launch_rows<kMX, false, 4, 2, 2, 4, kMX ? 2 : 3, 2>(g, s);
+}
+
 }  // namespace
 
-// Whether the rows are so few that the product streams weights for them.
-bool few_rows(const GroupedArgs& g) { return g.M <= 16 * g.E; }
+hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) { return launch_forward<false>(g, s); }
 
-hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) {
-  if (few_rows(g)) return launch_few_rows<false, 1, 4>(g, s);
-  return launch_rows<false, false, 4, 2, 2, 4, 3, 2>(g, s);
-}
-
-hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) {
-  if (few_rows(g)) return launch_few_rows<true, 1, 4>(g, s);
-  return launch_rows<true, false, 4, 2, 2, 4, 2, 2>(g, s);
-}
+hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) { return launch_forward<true>(g, s); }
 
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
+  if (g.kc <= 64) return launch_rows<false, true, 4, 1, 1, 4, 2, 2>(g, s);
+  if (few_tiles(g)) return launch_rows<false, true, 4, 2, 1, 4, 3, 3>(g, s);
   return launch_rows<false, true, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
+template <typename Out>
+hipError_t launch_weight_for(const GroupedArgs& g, hipStream_t s) {
+  if (g.nout <= 64) return launch_weight<Out, 2, 2, 2, 1, 2, 2>(g, s);
+  if (g.kc <= 64) return launch_weight<Out, 2, 2, 1, 4, 2, 2>(g, s);
+  return launch_weight<Out, 4, 2, 2, 4, 3, 2>(g, s);
+}
+
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
-  return fp32 ? launch_weight<float, 4, 2, 2, 4, 3, 2>(g, s) : launch_weight<uint16_t, 4, 2, 2, 4, 3, 2>(g, s);
+  return fp32 ? launch_weight_for<float>(g, s) : launch_weight_for<uint16_t>(g, s);
 }
 
 }  // namespace moeq
