@@ -949,6 +949,26 @@ def moeq_clip_grad_norm_workspace_bytes(count):
     return int(_load().moeq_clip_grad_norm_workspace_bytes(int(count)))
 
 
+_T = torch.Tensor
+
+
+def _gradients_ok(grads, outs):
+    """Whether grads and outs are what :func:`moeq_clip_grad_norm` takes, with
+    as little work per tensor as there can be (there may be hundreds)."""
+    if not all(isinstance(t, _T) for t in grads):
+        return False
+    dtypes = [g.dtype for g in grads]
+    devices = set(map(_T.get_device, grads))
+    ok = all(d in _GRAD_DTYPES for d in dtypes) and all(map(_T.is_contiguous, grads))
+    if outs is not grads:
+        if not all(isinstance(t, _T) for t in outs):
+            return False
+        devices.update(map(_T.get_device, outs))
+        ok = (ok and [o.dtype for o in outs] == dtypes and all(map(_T.is_contiguous, outs))
+              and [o.shape for o in outs] == [g.shape for g in grads])
+    return ok and len(devices) == 1 and min(devices) >= 0
+
+
 def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
     """The norm over all ``grads`` (bf16 and fp32 tensors of any shape) and
     ``grad * min(1, max_norm / norm)``, written in place or into ``out`` (one
@@ -961,18 +981,22 @@ def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError(f"out must hold {len(grads)} tensors, got {len(outs)}")
-    table = array.array("q")
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if not isinstance(g, torch.Tensor):
-            raise TypeError(f"grads[{i}] must be a torch tensor")
-        if g.dtype not in _GRAD_DTYPES:
-            raise TypeError(f"grads[{i}] must be torch.float32 or torch.bfloat16, got {g.dtype}")
-        if not g.is_contiguous():
-            raise ValueError(f"grads[{i}] must be contiguous")
-        if o is not g:
+    if not _gradients_ok(grads, outs):   # names what is wrong
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if not isinstance(g, torch.Tensor):
+                raise TypeError(f"grads[{i}] must be a torch tensor")
+            if g.dtype not in _GRAD_DTYPES:
+                raise TypeError(f"grads[{i}] must be torch.float32 or torch.bfloat16, got {g.dtype}")
+            if not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous")
             _dev(o, g.dtype, f"out[{i}]", g.shape)
-        table.extend((g.data_ptr(), o.data_ptr(), g.numel(), _GRAD_DTYPES[g.dtype]))
-    dev = _on_device("moeq_clip_grad_norm", *grads, *(outs if out is not None else []))
+        _on_device("moeq_clip_grad_norm", *grads, *outs)
+        raise ValueError("grads and out do not fit")
+    dev = grads[0].device
+    table = array.array("q")
+    for row in zip(map(_T.data_ptr, grads), map(_T.data_ptr, outs), map(_T.numel, grads),
+                   [_GRAD_DTYPES[g.dtype] for g in grads]):
+        table.extend(row)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     lib = _load()
     made = workspace is None
