@@ -169,35 +169,39 @@ struct Side {
   }
 };
 
-// Scale bytes of an MXFP4 row, eight per step, zeros past its end.  The loads
-// have no branch around them: past the row's last eight bytes those are read
-// and shifted down, and a row that is not there (or shorter than eight
-// blocks, whose only step first() loads) reads zeros.
-__device__ const uint64_t kNoScales = 0;
+// Scale bytes of an MXFP4 row, sixteen (those of two steps) at a time, zeros
+// past its end.  The loads have no branch around them: past the row's last
+// sixteen bytes those are read and shifted down, and a row that is not there
+// (or shorter than sixteen blocks, whose only pair first() loads) reads zeros.
+__device__ const uint64_t kNoScales[2] = {0, 0};
 struct ScaleRow {
   typedef __attribute__((address_space(1))) const uint8_t* Ptr;   // global, so that no load is a flat one
   Ptr p;
   int32_t n, lim;   // scales of the row; the last offset to load from
   __device__ __forceinline__ void init(const uint8_t* row, int n_) {
-    const bool in = row && n_ >= 8;
-    p = (Ptr)(in ? row : reinterpret_cast<const uint8_t*>(&kNoScales));
+    const bool in = row && n_ >= 16;
+    p = (Ptr)(in ? row : reinterpret_cast<const uint8_t*>(kNoScales));
     n = n_;
-    lim = in ? n_ - 8 : 0;
+    lim = in ? n_ - 16 : 0;
   }
-  __device__ __forceinline__ uint64_t load(int ks) const {
-    typedef uint64_t u64a __attribute__((aligned(1)));
-    return *(__attribute__((address_space(1))) const u64a*)(p + min(8 * ks, lim));
+  __device__ __forceinline__ u32x4 load(int pair) const {
+    typedef u32x4 u32x4a __attribute__((aligned(1)));
+    return *(__attribute__((address_space(1))) const u32x4a*)(p + min(16 * pair, lim));
   }
-  // what load(ks) returned, in place
-  __device__ __forceinline__ uint64_t use(uint64_t v, int ks) const {
-    const int half = 4 * min(max(8 * ks + 8 - n, 0), 8);
-    return (v >> half) >> half;
+  // what load(pair) returned, in place
+  __device__ __forceinline__ u32x4 use(u32x4 v, int pair) const {
+    const int half = 4 * min(max(16 * pair + 16 - n, 0), 16);
+    unsigned __int128 b = __builtin_bit_cast(unsigned __int128, v);
+    b = (b >> half) >> half;
+    return __builtin_bit_cast(u32x4, b);
   }
-  __device__ __forceinline__ static uint64_t first(const uint8_t* row, int n) {
-    uint64_t v = 0;
-    if (row)
-      for (int i = 0; i < n && i < 8; ++i) v |= (uint64_t)row[i] << (8 * i);
-    return v;
+  __device__ __forceinline__ static u32x4 first(const uint8_t* row, int n) {
+    uint64_t lo = 0, hi = 0;
+    if (row) {
+      for (int i = 0; i < min(n, 8); ++i) lo |= (uint64_t)row[i] << (8 * i);
+      for (int i = 8; i < min(n, 16); ++i) hi |= (uint64_t)row[i] << (8 * (i - 8));
+    }
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
   }
 };
 
@@ -211,7 +215,7 @@ struct Tile {
   using A = Side<kAT, kCols, kNW>;
   using B = Side<kBT, kRows, kNW>;
   static constexpr int kBytesB = kBufsA * A::kBytes;   // where the rows' buffers start
-  static constexpr int kScaleBuf = kMX ? 8 * 64 * kNW : 0;   // every thread stores a row's
+  static constexpr int kScaleBuf = kMX ? 16 * 64 * kNW : 0;   // every thread stores a row's
   static_assert(!kMX || kCols + kRows <= 64 * kNW, "a thread per scale row");
   static constexpr int kInstr = A::kInstr + B::kInstr;
   static constexpr int kScales = kBytesB + kBufsB * B::kBytes;   // and the scales'
@@ -225,15 +229,15 @@ struct Tile {
     const int wn = wave % kNWN, wm = wave / kNWN;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
     asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
-    char* sc = smem + kScales;   // MX: kCols then kRows rows of 8 B in each of two buffers
+    char* sc = smem + kScales;   // MX: kCols then kRows rows of 16 B (two steps) in each of two buffers
 
     // instruction i of step ks's copies into ring slot `slot`
     auto dma_a = [&](int ks, int slot, int i) { a.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(slot * A::kBytes)); };
     auto dma_b = [&](int ks, int slot, int i) {
       b.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(kBytesB + slot * B::kBytes));
     };
-    auto scale_store = [&](int buf, uint64_t v) {
-      *reinterpret_cast<uint64_t*>(sc + buf * kScaleBuf + 8 * t) = v;
+    auto scale_store = [&](int pair, u32x4 v) {
+      *reinterpret_cast<u32x4*>(sc + (pair & 1) * kScaleBuf + 16 * t) = v;
     };
     // the MFMA order is column block by column block: operand j of kOps is
     // the j-th that it needs (a 0, the b's, the other a's)
@@ -246,12 +250,13 @@ struct Tile {
         fa[n] = A::frag(ta, 32 * (kTN * wn + n), s, lane);
       }
     };
-    auto load_scales = [&](int buf, uint32_t (&sa)[kTN], uint32_t (&sb)[kTM]) {
-      const char* s0 = sc + buf * kScaleBuf + 8 * (lane & 31) + 4 * (lane >> 5);
+    // the dwords of step ks: scales 4 h .. 4 h + 3 of the lane's rows
+    auto load_scales = [&](int ks, uint32_t (&sa)[kTN], uint32_t (&sb)[kTM]) {
+      const char* s0 = sc + ((ks >> 1) & 1) * kScaleBuf + 16 * (lane & 31) + 8 * (ks & 1) + 4 * (lane >> 5);
 #pragma unroll
-      for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
+      for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 16 * 32 * (kTN * wn + n));
 #pragma unroll
-      for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
+      for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 16 * (kCols + 32 * (kTM * wm + m)));
     };
     // The step loop.  The barrier stands before the last MFMA step: by then
     // every wave holds that step's operands in registers, so that the LDS
@@ -265,11 +270,11 @@ struct Tile {
     // leave in flight whatever was issued after the next step's copies.
     constexpr int kInFlight = (kBufsA - 2) * A::kInstr + (kBufsB - 2) * B::kInstr;
     ScaleRow sr;
-    uint64_t sv = 0;   // scales on their way to LDS: those of step ks + 1
-    uint32_t sa[kTN], sb[kTM];
+    u32x4 sv = {0u, 0u, 0u, 0u};   // scales on their way to LDS: the next pair of steps'
+    uint32_t sa[2][kTN], sb[2][kTM];
     if constexpr (kMX) {
       sr.init(scales, nscale);
-      scale_store(0, nscale < 8 ? ScaleRow::first(scales, nscale) : sr.use(sr.load(0), 0));
+      scale_store(0, nscale < 16 ? ScaleRow::first(scales, nscale) : sr.use(sr.load(0), 0));
     }
     auto fill_a = [&](int p) {
 #pragma unroll
@@ -286,30 +291,29 @@ struct Tile {
       if (p < kBufsB) fill_b(p);
       if (kBufsA <= kBufsB && p < kBufsA - 1) fill_a(p);
     }
-    if constexpr (kMX) sv = sr.load(1);
     __builtin_amdgcn_s_waitcnt(kWaitLoads<kInFlight + B::kInstr>);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     u32x4 fa[2][kTN], fb[2][kTM];
 #pragma unroll
     for (int j = 0; j < kOps; ++j) frag(smem, smem + kBytesB, 0, j, fa[0], fb[0]);
-    if constexpr (kMX) load_scales(0, sa, sb);
+    if constexpr (kMX) load_scales(0, sa[0], sb[0]);
 
     int sa0 = 0, sb0 = 0;   // this step's ring slots
-    for (int ks = 0; ks < nks; ++ks) {
+    auto step = [&](auto parity, int ks) {   // parity: ks & 1 (MXFP4 only)
+      constexpr int kOdd = decltype(parity)::value;
       const int sa1 = sa0 + 1 == kBufsA ? 0 : sa0 + 1, sb1 = sb0 + 1 == kBufsB ? 0 : sb0 + 1;
       const int sap = sa0 == 0 ? kBufsA - 1 : sa0 - 1;
-      uint32_t na[kTN], nb[kTM];
+      if constexpr (kMX && !kOdd) sv = sr.load((ks >> 1) + 1);
 #pragma unroll
       for (int s = 0; s < kSub; ++s) {
         if (s + 1 == kSub) {
-          if constexpr (kMX) scale_store((ks + 1) & 1, sr.use(sv, ks + 1));
+          if constexpr (kMX && kOdd) scale_store((ks + 1) >> 1, sr.use(sv, (ks + 1) >> 1));
           __builtin_amdgcn_s_waitcnt(kWaitLoads<kInFlight>);
           __builtin_amdgcn_s_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
           if constexpr (kMX) {
-            load_scales((ks + 1) & 1, na, nb);
-            sv = sr.load(ks + 2);
+            load_scales(ks + 1, sa[kOdd ^ 1], sb[kOdd ^ 1]);
           }
         }
         const char* ta = smem + (s + 1 < kSub ? sa0 : sa1) * A::kBytes;
@@ -325,13 +329,17 @@ struct Tile {
               const i32x8 yb = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
               // operand formats 4: E2M1; scale byte s of the lanes' dwords
               if (s == 0)
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 0, sa[n], 0, sb[m]);
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    xa, yb, acc[n][m], 4, 4, 0, sa[kOdd][n], 0, sb[kOdd][m]);
               else if (s == 1)
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 1, sa[n], 1, sb[m]);
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    xa, yb, acc[n][m], 4, 4, 1, sa[kOdd][n], 1, sb[kOdd][m]);
               else if (s == 2)
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 2, sa[n], 2, sb[m]);
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    xa, yb, acc[n][m], 4, 4, 2, sa[kOdd][n], 2, sb[kOdd][m]);
               else
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, yb, acc[n][m], 4, 4, 3, sa[n], 3, sb[m]);
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+                    xa, yb, acc[n][m], 4, 4, 3, sa[kOdd][n], 3, sb[kOdd][m]);
             } else {
               acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fa[s & 1][n]),
                                                                   __builtin_bit_cast(bf16x8, fb[s & 1][m]),
@@ -355,15 +363,16 @@ struct Tile {
             __builtin_amdgcn_sched_barrier(0);
           }
       }
-      if constexpr (kMX) {
-#pragma unroll
-        for (int n = 0; n < kTN; ++n) sa[n] = na[n];
-#pragma unroll
-        for (int m = 0; m < kTM; ++m) sb[m] = nb[m];
-      }
       sa0 = sa1;
       sb0 = sb1;
-    }
+    };
+    int ks = 0;
+    if constexpr (kMX)
+      for (; ks + 1 < nks; ks += 2) {
+        step(std::integral_constant<int, 0>{}, ks);
+        step(std::integral_constant<int, 1>{}, ks + 1);
+      }
+    for (; ks < nks; ++ks) step(std::integral_constant<int, 0>{}, ks);
     __builtin_amdgcn_s_waitcnt(0);   // copies of steps past the end
     __syncthreads();
   }
@@ -762,7 +771,7 @@ bool streams(const GroupedArgs& g) { return g.M <= 16 * g.E || g.nout <= 32; }
 // half the columns then do better (and have room for a third buffer).
 bool few_tiles(const GroupedArgs& g) {
   const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
-  return rows * ((g.nout + 255) / 256) <= 256;
+  return rows * ((g.nout + 255) / 256) <= 128;
 }
 
 template <bool kMX>
