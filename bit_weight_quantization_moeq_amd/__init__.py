@@ -29,7 +29,7 @@ __all__ = [
     "moeq_stream_reference", "moeq_router_route", "moeq_experts_forward_routed", "Routing",
     "moeq_experts_forward_noalloc", "NOALLOC_SCRATCH_BYTES",
     "FMT_MXFP4", "MXFP4_BLOCKSIZE", "moeq_quantize_mxfp4", "moeq_grouped_mm", "moeq_grouped_mm_grad_input",
-    "moeq_grouped_mm_grad_weight", "moeq_grouped_mm_mxfp4", "moeq_clip_grad_norm_workspace_bytes",
+    "moeq_grouped_mm_grad_weight", "moeq_grouped_mm_grad_weight_workspace_bytes", "moeq_grouped_mm_mxfp4", "moeq_clip_grad_norm_workspace_bytes",
     "moeq_clip_grad_norm",
 ]
 
@@ -104,7 +104,8 @@ def _load():
         "moeq_dequantize_mxfp4": (I32, [QP, P, P]),
         "moeq_grouped_mm": (I32, [P, P, P, I32, I32, I32, I32, P, P]),
         "moeq_grouped_mm_grad_input": (I32, [P, P, P, I32, I32, I32, I32, P, P]),
-        "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P]),
+        "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
+        "moeq_grouped_mm_grad_weight_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "moeq_grouped_mm_mxfp4": (I32, [QP, QP, P, P, P]),
         "moeq_clip_grad_norm_workspace_bytes": (SZ, [I32]),
         "moeq_clip_grad_norm": (I32, [P, I32, ctypes.c_double, P, P, SZ, P]),
@@ -879,7 +880,13 @@ def moeq_grouped_mm_grad_input(grad_out, w, offsets, grad_x=None, stream=None):
     return dx
 
 
-def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_w=None, stream=None):
+def moeq_grouped_mm_grad_weight_workspace_bytes(M, E, N, K):
+    """Workspace bytes :func:`moeq_grouped_mm_grad_weight` needs (0 where no
+    expert's rows can be worth cutting into segments)."""
+    return int(_load().moeq_grouped_mm_grad_weight_workspace_bytes(int(M), int(E), int(N), int(K)))
+
+
+def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_w=None, workspace=None, stream=None):
     """Gradient of :func:`moeq_grouped_mm` with respect to ``w``:
     ``grad_w[e] = sum_p grad_out[p] x[p]^T`` over the expert's rows (zeros
     for an expert without rows), ``[E, N, K]`` in fp32 or bf16 (``dtype``, or
@@ -901,12 +908,17 @@ def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_
         raise TypeError(f"grad_w must be torch.float32 or torch.bfloat16, got {dtype}")
     dev = _on_device("moeq_grouped_mm_grad_weight", grad_out, x, offsets, grad_w)
     dw = torch.empty((E, N, K), dtype=dtype, device=dev) if grad_w is None else grad_w
+    lib = _load()
+    need = int(lib.moeq_grouped_mm_grad_weight_workspace_bytes(int(M), int(E), int(N), int(K)))
+    made = workspace is None and need > 0
+    if made or workspace is not None:
+        workspace = _workspace(workspace, need, dev)
     with _current(dev):
-        _check(_load().moeq_grouped_mm_grad_weight(_ptr(grad_out), _ptr(x), _ptr(offsets), int(M), int(E), int(N),
-                                                   int(K), _GRAD_DTYPES[dtype], _ptr(dw), _stream(stream, dev)),
+        _check(lib.moeq_grouped_mm_grad_weight(_ptr(grad_out), _ptr(x), _ptr(offsets), int(M), int(E), int(N), int(K),
+                                               _GRAD_DTYPES[dtype], _ptr(dw), _ptr(workspace),
+                                               workspace.numel() if workspace is not None else 0, _stream(stream, dev)),
                "moeq_grouped_mm_grad_weight")
-    if grad_w is None:
-        _used_on(stream, dw)
+    _used_on(stream, *([dw] if grad_w is None else []), *([workspace] if made else []))
     return dw
 
 

@@ -112,14 +112,26 @@ moeq_status moeq_grouped_mm_grad_input(const uint16_t* dy, const uint16_t* w, co
   return device_status(launch_grouped_mm_grad_input(g, static_cast<hipStream_t>(stream)));
 }
 
+size_t moeq_grouped_mm_grad_weight_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K) {
+  if (check_grouped(M, E, N, K) != MOEQ_OK) return 0;
+  return sizeof(float) * (size_t)grad_weight_slots(M, grad_weight_segment(M, E, N, K)) * N * K;
+}
+
 moeq_status moeq_grouped_mm_grad_weight(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int32_t M,
-                                        int32_t E, int32_t N, int32_t K, int32_t dtype, void* dw, void* stream) {
+                                        int32_t E, int32_t N, int32_t K, int32_t dtype, void* dw, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
   const moeq_status st = check_grouped(M, E, N, K);
   if (st != MOEQ_OK) return st;
   if (dtype != MOEQ_DTYPE_BF16 && dtype != MOEQ_DTYPE_FP32) return MOEQ_EFORMAT;
   if (!offsets || !dw || (M > 0 && (!dy || !x))) return MOEQ_EINVAL;
   if (!aligned16(dw) || (M > 0 && (!aligned16(dy) || !aligned16(x)))) return MOEQ_EALIGN;
-  const GroupedArgs g = {x, dy, nullptr, nullptr, offsets, dw, M, E, N, K};
+  const size_t need = moeq_grouped_mm_grad_weight_workspace_bytes(M, E, N, K);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOEQ_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return MOEQ_EALIGN;
+  GroupedArgs g = {x, dy, nullptr, nullptr, offsets, dw, M, E, N, K};
+  g.segment = grad_weight_segment(M, E, N, K);
+  g.slots = (int32_t)grad_weight_slots(M, g.segment);
+  g.partial = static_cast<float*>(workspace);
   return device_status(launch_grouped_mm_grad_weight(g, dtype == MOEQ_DTYPE_FP32, static_cast<hipStream_t>(stream)));
 }
 

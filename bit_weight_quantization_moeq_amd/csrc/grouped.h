@@ -23,7 +23,13 @@ struct GroupedArgs {
   const int32_t* offsets;  // [E + 1], on the device
   void* out;
   int32_t M, E, nout, kc;
+  // grad_weight: rows per segment, and room for the fp32 sums of the segments
+  // of experts that have several
+  int32_t segment = 0, slots = 0;
+  float* partial = nullptr;
 };
+int32_t grad_weight_segment(int32_t M, int32_t E, int32_t N, int32_t K);
+int64_t grad_weight_slots(int32_t M, int32_t segment);   // [N][K] slots of the workspace
 hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s);
 hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s);
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s);

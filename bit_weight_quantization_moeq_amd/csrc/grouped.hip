@@ -377,6 +377,39 @@ struct Tile {
     __syncthreads();
   }
 
+  // The same for a contraction of one step at most (bf16, one buffer each):
+  // the product moves its output and little else, so the tile is kept small
+  // enough for four workgroups per compute unit, whose copies, products and
+  // stores overlap.
+  __device__ __forceinline__ static void run_short(char* smem, const A& a, const B& b, int kbytes, f32x16 (&acc)[kTN][kTM]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave % kNWN, wm = wave / kNWN;
+    uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
+    asm volatile("" : "+s"(lds0));
+#pragma unroll
+    for (int i = 0; i < A::kInstr; ++i) a.template dma<false>(0, i, wave, lds0);
+#pragma unroll
+    for (int i = 0; i < B::kInstr; ++i) b.template dma<false>(0, i, wave, lds0 + (uint32_t)kBytesB);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    // MFMA step s covers chunks s and 4 + s: none behind the contraction's end
+    const int steps = min(kSub, kbytes / 16);
+    for (int s = 0; s < steps; ++s) {
+      u32x4 fa[kTN], fb[kTM];
+#pragma unroll
+      for (int n = 0; n < kTN; ++n) fa[n] = A::frag(smem, 32 * (kTN * wn + n), s, lane);
+#pragma unroll
+      for (int m = 0; m < kTM; ++m) fb[m] = B::frag(smem + kBytesB, 32 * (kTM * wm + m), s, lane);
+#pragma unroll
+      for (int n = 0; n < kTN; ++n)
+#pragma unroll
+        for (int m = 0; m < kTM; ++m)
+          acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fa[n]),
+                                                              __builtin_bit_cast(bf16x8, fb[m]), acc[n][m], 0, 0, 0);
+    }
+    __syncthreads();
+  }
+
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
   // out, ld elements a row, staged through LDS so that the stores write whole
   // rows (from the accumulator layout one instruction would touch 32 rows),
@@ -526,12 +559,15 @@ __device__ __forceinline__ void rows_tile(char* smem, const GroupedArgs& g, int 
   for (int n = 0; n < kTN; ++n)
 #pragma unroll
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
-  T::run(smem, a, b, scales, nscale, (kbytes + kStepBytes - 1) / kStepBytes, acc);
+  if constexpr (kBufsA == 1)
+    T::run_short(smem, a, b, kbytes, acc);
+  else
+    T::run(smem, a, b, scales, nscale, (kbytes + kStepBytes - 1) / kStepBytes, acc);
   T::store(smem, acc, static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.nout + c0, g.nout, nrows, ncols);
 }
 
 template <bool kMX, bool kAT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
-__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void rows_kernel(GroupedArgs g) {
+__global__ __launch_bounds__(64 * kNWN * kNWM, kBufsA == 1 ? 4 : kNWN * kNWM / 4) void rows_kernel(GroupedArgs g) {
   using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[imax(Big::kLds, Big::out_bytes(2))];
   int e, row0, nrows, ct;
@@ -547,25 +583,68 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void rows_kernel
   rows_tile<kMX, kAT, kNWN, kNWM, kTN, 1, kBufsA, kBufsB>(smem, g, e, row0, nrows, c0);
 }
 
-// grad_weight: tile of dw[e] [N][K]: rows n (dy columns, B), columns k (x
-// columns, A), contraction over the expert's rows.
+// grad_weight.  An expert's rows are cut into segments of g.segment rows (one
+// at least, also for an expert without rows, whose result is zeros), so that a
+// long expert is not one workgroup's chain of steps.  The only segment of an
+// expert writes dw; several write fp32 partial sums, one [N][K] slot of the
+// workspace each, which sum_segments_kernel adds in order.
+
+// Work item of this workgroup among the (segment, tile) pairs, tiles a
+// segment, segment by segment, every XCD a contiguous range: its expert, tile
+// r, segment k of the expert's nseg, and the slots before the expert's.
+// Experts of one segment have no slots.
+__device__ __forceinline__ bool find_segment(const int32_t* offsets, int E, int M, int segment, int tiles, int& e, int& r,
+                                             int& k, int& nseg, int& slot) {
+  const int lane = threadIdx.x & 63;
+  auto segments = [&](int i) {
+    int lo, n;
+    if (i >= E) return 0;
+    expert_rows(offsets, i, M, lo, n);
+    return max((n + segment - 1) / segment, 1);
+  };
+  int total = 0;
+  for (int i = 0; i < E; i += 64) total += __builtin_amdgcn_readlane(wave_scan(segments(i + lane)), 63);
+  total *= tiles;
+  const int per = (total + kXcds - 1) / kXcds, w = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if ((int)blockIdx.x / kXcds >= per || w >= total) return false;
+  const int at = w / tiles;
+  r = w - at * tiles;
+  int before = 0, slots = 0;
+  for (int i = 0; i < E; i += 64) {
+    const int ns = segments(i + lane), sl = ns > 1 ? ns : 0;
+    const int incl = wave_scan(ns), slot_incl = wave_scan(sl), first = before + incl - ns;
+    const uint64_t hit = __ballot(at >= first && at < first + ns);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      e = i + src;
+      k = at - __builtin_amdgcn_readlane(first, src);
+      nseg = __builtin_amdgcn_readlane(ns, src);
+      slot = slots + __builtin_amdgcn_readlane(slot_incl - sl, src);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+    slots += __builtin_amdgcn_readlane(slot_incl, 63);
+  }
+  return false;
+}
+
+// Tile of a segment's product [N][K]: rows n (dy columns, B), columns k (x
+// columns, A), contraction over the segment's rows.
 template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void weight_kernel(GroupedArgs g) {
   using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
-  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(sizeof(Out)))];
+  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(4))];
   const int N = g.nout, K = g.kc;
   const int nk = (K + T::kCols - 1) / T::kCols, nn = (N + T::kRows - 1) / T::kRows;
-  const int total = g.E * nn * nk, per = (total + kXcds - 1) / kXcds;
-  const int slot = blockIdx.x / kXcds, w = (blockIdx.x % kXcds) * per + slot;
-  if (slot >= per || w >= total) return;
-  const int e = w / (nn * nk), r = w - e * nn * nk;
+  int e, r, seg, nseg, slot;
+  if (!find_segment(g.offsets, g.E, g.M, g.segment, nn * nk, e, r, seg, nseg, slot)) return;
   // row tiles in groups, as in find_tile
   const int grp = r / (kTileGroup * nk), gt = min(kTileGroup, nn - grp * kTileGroup), rr = r - grp * kTileGroup * nk;
   const int k0 = (rr / gt) * T::kCols, n0 = (grp * kTileGroup + rr % gt) * T::kRows;
   int lo, cnt;
   expert_rows(g.offsets, e, g.M, lo, cnt);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  cnt = __builtin_amdgcn_readfirstlane(cnt);
+  lo = __builtin_amdgcn_readfirstlane(lo) + seg * g.segment;
+  cnt = min(__builtin_amdgcn_readfirstlane(cnt) - seg * g.segment, g.segment);
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   typename T::A a;
   typename T::B b;
@@ -577,8 +656,48 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void weight_kern
 #pragma unroll
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
   T::run(smem, a, b, nullptr, 0, (cnt + 63) / 64, acc);
-  T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)e * N + n0) * K + k0, K, min(T::kRows, N - n0),
-           min(T::kCols, K - k0));
+  const int nrows = min(T::kRows, N - n0), ncols = min(T::kCols, K - k0);
+  if (nseg == 1)
+    T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)e * N + n0) * K + k0, K, nrows, ncols);
+  else if (slot + nseg <= g.slots)
+    T::store(smem, acc, g.partial + ((int64_t)(slot + seg) * N + n0) * K + k0, K, nrows, ncols);
+}
+
+// dw of the blockIdx.y-th expert of several segments: their sums, in order.
+template <typename Out>
+__global__ __launch_bounds__(256) void sum_segments_kernel(GroupedArgs g) {
+  const int lane = threadIdx.x & 63;
+  int e = -1, nseg = 0, slot = 0;
+  for (int i = 0, many = 0, slots = 0; i < g.E; i += 64) {
+    int lo = 0, n = 0;
+    if (i + lane < g.E) expert_rows(g.offsets, i + lane, g.M, lo, n);
+    const int ns = (n + g.segment - 1) / g.segment, sl = ns > 1 ? ns : 0;
+    const int rank = wave_scan(ns > 1 ? 1 : 0), slot_incl = wave_scan(sl);
+    const uint64_t hit = __ballot(ns > 1 && many + rank - 1 == (int)blockIdx.y);
+    if (hit) {
+      const int src = __builtin_ctzll(hit);
+      e = i + src;
+      nseg = __builtin_amdgcn_readlane(ns, src);
+      slot = slots + __builtin_amdgcn_readlane(slot_incl - sl, src);
+      break;
+    }
+    many += __builtin_amdgcn_readlane(rank, 63);
+    slots += __builtin_amdgcn_readlane(slot_incl, 63);
+  }
+  if (e < 0 || slot + nseg > g.slots) return;
+  const int64_t nk4 = (int64_t)g.nout * g.kc / 4;   // (K % 8 == 0)
+  const float4* p = reinterpret_cast<const float4*>(g.partial) + slot * nk4;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < nk4; i += (int64_t)gridDim.x * 256) {
+    float4 s = p[i];
+    for (int k = 1; k < nseg; ++k) {
+      const float4 v = p[k * nk4 + i];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    if constexpr (sizeof(Out) == 4)
+      reinterpret_cast<float4*>(g.out)[e * nk4 + i] = s;
+    else
+      reinterpret_cast<uint2*>(g.out)[e * nk4 + i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -756,12 +875,11 @@ hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
 template <typename Out, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
   using T = Tile<false, true, true, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
-  const int64_t total = (int64_t)g.E * ((g.nout + T::kRows - 1) / T::kRows) * ((g.kc + T::kCols - 1) / T::kCols);
-  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
+  const int64_t tiles = (int64_t)((g.nout + T::kRows - 1) / T::kRows) * ((g.kc + T::kCols - 1) / T::kCols);
+  const int64_t grid = ((g.E + g.M / g.segment) * tiles + kXcds - 1) / kXcds * kXcds;
   weight_kernel<Out, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
   return hipGetLastError();
 }
-
 
 // Whether the product does little more than stream one operand past the other:
 // few rows per expert (the weights), or few output columns (the rows).
@@ -777,6 +895,8 @@ bool few_tiles(const GroupedArgs& g) {
 template <bool kMX>
 hipError_t launch_forward(const GroupedArgs& g, hipStream_t s) {
   if (streams(g)) return launch_few_rows<kMX, 1, 4>(g, s);
+  if constexpr (!kMX)
+    if (g.kc <= 64) return launch_rows<false, false, 4, 1, 1, 2, 1, 1>(g, s);
   if (few_tiles(g)) return launch_rows<kMX, false, 4, 2, 1, 4, 3, 3>(g, s);
   // (three buffers of the columns' operand leave no room for the scales)
   return launch_rows<kMX, false, 4, 2, 2, 4, kMX ? 2 : 3, 2>(g, s);
@@ -789,17 +909,51 @@ hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s) { return launc
 hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s) { return launch_forward<true>(g, s); }
 
 hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
-  if (g.kc <= 64) return launch_rows<false, true, 4, 1, 1, 4, 2, 2>(g, s);
+  if (g.kc <= 64) return launch_rows<false, true, 4, 1, 1, 2, 1, 1>(g, s);
   if (few_tiles(g)) return launch_rows<false, true, 4, 2, 1, 4, 3, 3>(g, s);
   return launch_rows<false, true, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
+namespace {
+
+// Tile shapes of grad_weight: narrow outputs take tiles that are narrow, too
+// (and more of them on a compute unit).
+enum class WeightTile { kSquare, kFewRows, kFewCols };
+WeightTile weight_tile(int32_t N, int32_t K) {
+  return N <= 64 ? WeightTile::kFewRows : K <= 64 ? WeightTile::kFewCols : WeightTile::kSquare;
+}
+
 template <typename Out>
 hipError_t launch_weight_for(const GroupedArgs& g, hipStream_t s) {
-  if (g.nout <= 64) return launch_weight<Out, 2, 2, 2, 1, 2, 2>(g, s);
-  if (g.kc <= 64) return launch_weight<Out, 2, 2, 1, 4, 2, 2>(g, s);
-  return launch_weight<Out, 4, 2, 2, 4, 3, 2>(g, s);
+  hipError_t e;
+  switch (weight_tile(g.nout, g.kc)) {
+    case WeightTile::kFewRows: e = launch_weight<Out, 2, 2, 2, 1, 2, 2>(g, s); break;
+    case WeightTile::kFewCols: e = launch_weight<Out, 2, 2, 1, 4, 2, 2>(g, s); break;
+    default: e = launch_weight<Out, 4, 2, 2, 4, 3, 2>(g, s);
+  }
+  const int32_t many = g.M / g.segment;   // experts of more than one segment, at most
+  if (e != hipSuccess || many == 0) return e;
+  const int64_t blocks = ((int64_t)g.nout * g.kc / 4 + 255) / 256;
+  sum_segments_kernel<Out><<<dim3((unsigned)std::min<int64_t>(blocks, 1024), (unsigned)many), 256, 0, s>>>(g);
+  return hipGetLastError();
 }
+
+}  // namespace
+
+int32_t grad_weight_segment(int32_t M, int32_t E, int32_t N, int32_t K) {
+  // Enough segments to fill the card when every expert had one (1024 narrow
+  // or 256 square tiles), of at least 512 rows: eight steps, so that a slot's
+  // traffic stays below that of the rows.
+  (void)E;
+  const WeightTile w = weight_tile(N, K);
+  const int64_t rows = w == WeightTile::kFewRows ? 64 : 256, cols = w == WeightTile::kFewRows ? 128 : w == WeightTile::kFewCols ? 64 : 256;
+  const int64_t tiles = ((N + rows - 1) / rows) * ((K + cols - 1) / cols);
+  const int64_t want = std::max<int64_t>(1, (w == WeightTile::kSquare ? 256 : 1024) / tiles);
+  const int64_t len = std::max<int64_t>(512, (M + want - 1) / want);
+  return (int32_t)((len + 63) / 64 * 64);
+}
+
+int64_t grad_weight_slots(int32_t M, int32_t segment) { return 2 * (int64_t)(M / segment); }
 
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
   return fp32 ? launch_weight_for<float>(g, s) : launch_weight_for<uint16_t>(g, s);

@@ -453,6 +453,9 @@ moeq_status moeq_dequantize_mxfp4(const moeq_qweight *src, uint16_t *out_bf16, v
  *                  [E][N][K]; zeros for an expert without rows
  *   offsets        int32 [E+1] on the device, ascending, as
  *                  moeq_route_buckets and moeq_router_route write them
+ *   workspace      of moeq_grouped_mm_grad_weight_workspace_bytes(M, E, N, K),
+ *                  16-byte aligned: the rows of an expert that has many are
+ *                  summed in segments (none, and NULL, where that is 0)
  * Products of bf16 values summed in fp32, rounded once at the end; the same
  * bits from run to run.  Rows of out and grad_x outside [offsets[0],
  * offsets[E]) are not written, and rows outside an expert's range never
@@ -470,7 +473,8 @@ moeq_status moeq_grouped_mm_grad_input(const uint16_t *grad_out_bf16, const uint
                                        void *stream);
 moeq_status moeq_grouped_mm_grad_weight(const uint16_t *grad_out_bf16, const uint16_t *x_bf16, const int32_t *offsets,
                                         int32_t M, int32_t E, int32_t N, int32_t K, int32_t dtype, void *grad_w,
-                                        void *stream);
+                                        void *workspace, size_t workspace_bytes, void *stream);
+size_t moeq_grouped_mm_grad_weight_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K);
 
 /*
  * moeq_grouped_mm with both operands in MXFP4: x one "expert" of M rows

@@ -113,6 +113,31 @@ def test_forward_and_gradients(rows, N, K):
         assert not dw[e].any()
 
 
+@pytest.mark.parametrize("N,K", [(16, 264), (264, 16), (264, 264)])
+@pytest.mark.parametrize("sizes", [[1500], [0, 513, 1, 512, 2050, 0, 700], [40] * 70 + [1100]])
+def test_gradient_of_long_experts_is_summed_in_segments(N, K, sizes):
+    """Segments of 512 rows (more for the square tile): partial sums in fp32,
+    added in fp32, so the bound of one long sum holds."""
+    say(f"grouped segments {N} {K} {len(sizes)}")
+    g = torch.Generator(device=DEV).manual_seed(21)
+    off = _offsets(sizes, 3)
+    M = int(off[-1]) + 2
+    x = torch.randn((M, K), generator=g, device=DEV).to(torch.bfloat16)
+    dy = torch.randn((M, N), generator=g, device=DEV).to(torch.bfloat16)
+    for t in (x, dy):
+        t[:3], t[-2:] = float("nan"), float("nan")
+    doff = torch.from_numpy(off).to(DEV)
+    xs, dys = _clean(x, off), _clean(dy, off)
+    want, mag = grouped_mm_grad_weight(dys, xs, off), grouped_mm_grad_weight(np.abs(dys), np.abs(xs), off)
+    ws = torch.full((moeq.moeq_grouped_mm_grad_weight_workspace_bytes(M, len(sizes), N, K) + 64,), 0xff,
+                    dtype=torch.uint8, device=DEV)   # NaNs, where the call does not write
+    for dtype, half in ((torch.float32, 2.0 ** -24), (torch.bfloat16, 2.0 ** -8)):
+        dw = moeq.moeq_grouped_mm_grad_weight(dy, x, doff, dtype=dtype, workspace=ws)
+        _assert_close(dw, want, mag, max(sizes), half)
+        assert (ws[-64:] == 0xff).all()
+        assert torch.equal(dw, moeq.moeq_grouped_mm_grad_weight(dy, x, doff, dtype=dtype))
+
+
 def _mx_random(shape, g):
     codes = torch.randint(0, 256, (*shape[:-1], shape[-1] // 2), generator=g, device=DEV, dtype=torch.uint8)
     scales = torch.randint(120, 134, (*shape[:-1], shape[-1] // 32), generator=g, device=DEV, dtype=torch.uint8)

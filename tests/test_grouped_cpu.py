@@ -166,8 +166,13 @@ def test_library_refuses_grouped_before_any_device_call():
     assert dx(N=12) == -2 and dx(dy=0) == -1 and dx(dy=4104) == -5 and dx(M=0) == 0
     assert dx(M=1 << 28, K=1 << 16) == -2
 
-    def dw(M=4, E=2, N=16, K=24, dtype=2, out=4096, x=4096):
-        return lib.moeq_grouped_mm_grad_weight(P(4096), P(x), P(4096), M, E, N, K, dtype, P(out), None)
+    def dw(M=4, E=2, N=16, K=24, dtype=2, out=4096, x=4096, ws=0, nbytes=0):
+        return lib.moeq_grouped_mm_grad_weight(P(4096), P(x), P(4096), M, E, N, K, dtype, P(out), P(ws), nbytes, None)
+
+    need = lib.moeq_grouped_mm_grad_weight_workspace_bytes
+    assert need(4, 2, 16, 24) == 0 and need(1 << 20, 2, 16, 24) > 0 and need(1 << 20, 2, 16, 20) == 0
+    assert dw(M=1 << 20) == -6 and dw(M=1 << 20, ws=4096, nbytes=64) == -6
+    assert dw(M=1 << 20, ws=4100, nbytes=need(1 << 20, 2, 16, 24)) == -5
 
     assert dw(dtype=3) == -4 and dw(out=0) == -1 and dw(out=4104) == -5 and dw(K=20) == -2 and dw(x=0) == -1
 
