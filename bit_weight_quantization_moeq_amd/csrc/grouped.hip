@@ -462,12 +462,6 @@ struct Tile {
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
 
-// Rows [lo, hi) of expert e, in range whatever offsets hold.
-__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int M, int& lo, int& n) {
-  lo = min(max(offsets[e], 0), M);
-  n = max(min(offsets[e + 1], M) - lo, 0);
-}
-
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int add_dpp(int v) {
   return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
@@ -482,49 +476,75 @@ __device__ __forceinline__ int wave_scan(int v) {
   return add_dpp<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
 }
 
+// The experts' row ranges, 64 experts at a time, one per lane.  The first 256
+// are loaded together (one memory latency for all that is needed of them);
+// visit(f) calls f(first expert of the 64, lo, rows) in order until it returns
+// true, and says whether it did.
+struct ExpertRows {
+  static constexpr int kKept = 4;
+  const int32_t* offsets;
+  int32_t E, M;
+  int lo[kKept], n[kKept];
+  __device__ __forceinline__ void rows(int i, int& l, int& c) const {   // none past the last expert
+    l = min(max(offsets[min(i, E)], 0), M);
+    c = max(min(offsets[min(i + 1, E)], M) - l, 0);
+  }
+  __device__ __forceinline__ ExpertRows(const GroupedArgs& g) : offsets(g.offsets), E(g.E), M(g.M) {
+#pragma unroll
+    for (int c = 0; c < kKept; ++c) rows(64 * c + (threadIdx.x & 63), lo[c], n[c]);
+  }
+  template <typename F>
+  __device__ __forceinline__ bool visit(F f) const {
+#pragma unroll
+    for (int c = 0; c < kKept; ++c)
+      if (64 * c < E && f(64 * c, lo[c], n[c])) return true;
+    for (int i = 64 * kKept; i < E; i += 64) {
+      int l, c;
+      rows(i + (threadIdx.x & 63), l, c);
+      if (f(i, l, c)) return true;
+    }
+    return false;
+  }
+};
+
 // Work item of this workgroup among the (expert, row tile, column tile)
 // triples, expert-major; every XCD takes a contiguous range, so that the
 // tiles that share an expert's weights and rows share an L2.  An expert's
 // rows are cut into ceil(rows / max_rows) near-equal tiles, taken in groups
 // of kTileGroup that go through the column tiles together.  Each wave scans
 // the experts by itself, 64 at a time.
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int M, int max_rows, int ncol, int& e, int& row0,
-                                          int& nrows, int& ct) {
-  const int lane = threadIdx.x & 63;
-  auto tiles = [&](int i, int& lo, int& n) {
-    lo = n = 0;
-    if (i < E) expert_rows(offsets, i, M, lo, n);
-    return (n + max_rows - 1) / max_rows;
-  };
-  int lo, n, total = 0;
-  for (int i = 0; i < E; i += 64) total += __builtin_amdgcn_readlane(wave_scan(tiles(i + lane, lo, n)), 63);
+__device__ __forceinline__ bool find_tile(const GroupedArgs& g, int max_rows, int ncol, int& e, int& row0, int& nrows,
+                                          int& ct) {
+  const ExpertRows x(g);
+  int total = 0;
+  x.visit([&](int, int, int n) {
+    total += __builtin_amdgcn_readlane(wave_scan((n + max_rows - 1) / max_rows), 63);
+    return false;
+  });
   total *= ncol;
   const int per = (total + kXcds - 1) / kXcds;
   const int slot = blockIdx.x / kXcds, w = (blockIdx.x % kXcds) * per + slot;
   if (slot >= per || w >= total) return false;
   int before = 0;
-  for (int i = 0; i < E; i += 64) {
-    const int nt = tiles(i + lane, lo, n);
-    const int incl = wave_scan(nt);
+  return x.visit([&](int i, int lo, int n) {
+    const int nt = (n + max_rows - 1) / max_rows, incl = wave_scan(nt);
     const int first = before + incl - nt;
     const uint64_t hit = __ballot(w >= first * ncol && w < (first + nt) * ncol);
-    if (hit) {
-      const int src = __builtin_ctzll(hit);
-      e = i + src;
-      const int f = __builtin_amdgcn_readlane(first, src), k = __builtin_amdgcn_readlane(nt, src);
-      const int r0 = __builtin_amdgcn_readlane(lo, src), c = __builtin_amdgcn_readlane(n, src);
-      const int r = w - f * ncol, g = r / (kTileGroup * ncol), gt = min(kTileGroup, k - g * kTileGroup);
-      const int rr = r - g * kTileGroup * ncol;
-      ct = rr / gt;
-      const int mt = g * kTileGroup + (rr - ct * gt);
-      const int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
-      row0 = r0 + a;
-      nrows = b - a;
-      return true;
-    }
     before += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
+    if (!hit) return false;
+    const int src = __builtin_ctzll(hit);
+    e = i + src;
+    const int f = __builtin_amdgcn_readlane(first, src), k = __builtin_amdgcn_readlane(nt, src);
+    const int r0 = __builtin_amdgcn_readlane(lo, src), c = __builtin_amdgcn_readlane(n, src);
+    const int r = w - f * ncol, grp = r / (kTileGroup * ncol), gt = min(kTileGroup, k - grp * kTileGroup);
+    const int rr = r - grp * kTileGroup * ncol;
+    ct = rr / gt;
+    const int mt = grp * kTileGroup + (rr - ct * gt);
+    const int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
+    row0 = r0 + a;
+    nrows = b - a;
+    return true;
+  });
 }
 
 // forward (kAT = false, kMX or not) and grad_input (kAT = true).
@@ -571,7 +591,7 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kBufsA == 1 ? 4 : kNWN * kNWM / 4
   using Big = Tile<kMX, kAT, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[imax(Big::kLds, Big::out_bytes(2))];
   int e, row0, nrows, ct;
-  if (!find_tile(g.offsets, g.E, g.M, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
+  if (!find_tile(g, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
   const int c0 = ct * Big::kCols;
   // blocks of 32 rows per wave: as few as the tile's rows need
   if constexpr (kTM > 3)
@@ -590,42 +610,45 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kBufsA == 1 ? 4 : kNWN * kNWM / 4
 // workspace each, which sum_segments_kernel adds in order.
 
 // Work item of this workgroup among the (segment, tile) pairs, tiles a
-// segment, segment by segment, every XCD a contiguous range: its expert, tile
-// r, segment k of the expert's nseg, and the slots before the expert's.
-// Experts of one segment have no slots.
-__device__ __forceinline__ bool find_segment(const int32_t* offsets, int E, int M, int segment, int tiles, int& e, int& r,
-                                             int& k, int& nseg, int& slot) {
+// segment, segment by segment, every XCD a contiguous range: its expert, rows
+// [lo, lo + n), tile r, segment k of the expert's nseg, and the slots before
+// the expert's.  Experts of one segment have no slots.
+struct Segment {
+  int e, lo, n, r, k, nseg, slot;
+};
+__device__ __forceinline__ bool find_segment(const GroupedArgs& g, int tiles, Segment& o) {
+  const ExpertRows x(g);
   const int lane = threadIdx.x & 63;
-  auto segments = [&](int i) {
-    int lo, n;
-    if (i >= E) return 0;
-    expert_rows(offsets, i, M, lo, n);
-    return max((n + segment - 1) / segment, 1);
-  };
+  auto segments = [&](int i, int n) { return i + lane < g.E ? max((n + g.segment - 1) / g.segment, 1) : 0; };
   int total = 0;
-  for (int i = 0; i < E; i += 64) total += __builtin_amdgcn_readlane(wave_scan(segments(i + lane)), 63);
+  x.visit([&](int i, int, int n) {
+    total += __builtin_amdgcn_readlane(wave_scan(segments(i, n)), 63);
+    return false;
+  });
   total *= tiles;
   const int per = (total + kXcds - 1) / kXcds, w = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
   if ((int)blockIdx.x / kXcds >= per || w >= total) return false;
   const int at = w / tiles;
-  r = w - at * tiles;
+  o.r = w - at * tiles;
   int before = 0, slots = 0;
-  for (int i = 0; i < E; i += 64) {
-    const int ns = segments(i + lane), sl = ns > 1 ? ns : 0;
+  return x.visit([&](int i, int lo, int n) {
+    const int ns = segments(i, n), sl = ns > 1 ? ns : 0;
     const int incl = wave_scan(ns), slot_incl = wave_scan(sl), first = before + incl - ns;
     const uint64_t hit = __ballot(at >= first && at < first + ns);
     if (hit) {
       const int src = __builtin_ctzll(hit);
-      e = i + src;
-      k = at - __builtin_amdgcn_readlane(first, src);
-      nseg = __builtin_amdgcn_readlane(ns, src);
-      slot = slots + __builtin_amdgcn_readlane(slot_incl - sl, src);
+      o.e = i + src;
+      o.k = at - __builtin_amdgcn_readlane(first, src);
+      o.nseg = __builtin_amdgcn_readlane(ns, src);
+      o.slot = slots + __builtin_amdgcn_readlane(slot_incl - sl, src);
+      o.lo = __builtin_amdgcn_readlane(lo, src) + o.k * g.segment;
+      o.n = min(__builtin_amdgcn_readlane(n, src) - o.k * g.segment, g.segment);
       return true;
     }
     before += __builtin_amdgcn_readlane(incl, 63);
     slots += __builtin_amdgcn_readlane(slot_incl, 63);
-  }
-  return false;
+    return false;
+  });
 }
 
 // Tile of a segment's product [N][K]: rows n (dy columns, B), columns k (x
@@ -636,15 +659,12 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void weight_kern
   __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(4))];
   const int N = g.nout, K = g.kc;
   const int nk = (K + T::kCols - 1) / T::kCols, nn = (N + T::kRows - 1) / T::kRows;
-  int e, r, seg, nseg, slot;
-  if (!find_segment(g.offsets, g.E, g.M, g.segment, nn * nk, e, r, seg, nseg, slot)) return;
+  Segment sg;
+  if (!find_segment(g, nn * nk, sg)) return;
+  const int lo = sg.lo, cnt = sg.n, r = sg.r;
   // row tiles in groups, as in find_tile
   const int grp = r / (kTileGroup * nk), gt = min(kTileGroup, nn - grp * kTileGroup), rr = r - grp * kTileGroup * nk;
   const int k0 = (rr / gt) * T::kCols, n0 = (grp * kTileGroup + rr % gt) * T::kRows;
-  int lo, cnt;
-  expert_rows(g.offsets, e, g.M, lo, cnt);
-  lo = __builtin_amdgcn_readfirstlane(lo) + seg * g.segment;
-  cnt = min(__builtin_amdgcn_readfirstlane(cnt) - seg * g.segment, g.segment);
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   typename T::A a;
   typename T::B b;
@@ -657,20 +677,18 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void weight_kern
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
   T::run(smem, a, b, nullptr, 0, (cnt + 63) / 64, acc);
   const int nrows = min(T::kRows, N - n0), ncols = min(T::kCols, K - k0);
-  if (nseg == 1)
-    T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)e * N + n0) * K + k0, K, nrows, ncols);
-  else if (slot + nseg <= g.slots)
-    T::store(smem, acc, g.partial + ((int64_t)(slot + seg) * N + n0) * K + k0, K, nrows, ncols);
+  if (sg.nseg == 1)
+    T::store(smem, acc, static_cast<Out*>(g.out) + ((int64_t)sg.e * N + n0) * K + k0, K, nrows, ncols);
+  else if (sg.slot + sg.nseg <= g.slots)
+    T::store(smem, acc, g.partial + ((int64_t)(sg.slot + sg.k) * N + n0) * K + k0, K, nrows, ncols);
 }
 
 // dw of the blockIdx.y-th expert of several segments: their sums, in order.
 template <typename Out>
 __global__ __launch_bounds__(256) void sum_segments_kernel(GroupedArgs g) {
-  const int lane = threadIdx.x & 63;
-  int e = -1, nseg = 0, slot = 0;
-  for (int i = 0, many = 0, slots = 0; i < g.E; i += 64) {
-    int lo = 0, n = 0;
-    if (i + lane < g.E) expert_rows(g.offsets, i + lane, g.M, lo, n);
+  const ExpertRows x(g);
+  int e = -1, nseg = 0, slot = 0, many = 0, slots = 0;
+  x.visit([&](int i, int, int n) {
     const int ns = (n + g.segment - 1) / g.segment, sl = ns > 1 ? ns : 0;
     const int rank = wave_scan(ns > 1 ? 1 : 0), slot_incl = wave_scan(sl);
     const uint64_t hit = __ballot(ns > 1 && many + rank - 1 == (int)blockIdx.y);
@@ -679,11 +697,12 @@ __global__ __launch_bounds__(256) void sum_segments_kernel(GroupedArgs g) {
       e = i + src;
       nseg = __builtin_amdgcn_readlane(ns, src);
       slot = slots + __builtin_amdgcn_readlane(slot_incl - sl, src);
-      break;
+      return true;
     }
     many += __builtin_amdgcn_readlane(rank, 63);
     slots += __builtin_amdgcn_readlane(slot_incl, 63);
-  }
+    return false;
+  });
   if (e < 0 || slot + nseg > g.slots) return;
   const int64_t nk4 = (int64_t)g.nout * g.kc / 4;   // (K % 8 == 0)
   const float4* p = reinterpret_cast<const float4*>(g.partial) + slot * nk4;
@@ -746,7 +765,7 @@ __global__ __launch_bounds__(64 * kNW) void few_rows_kernel(GroupedArgs g, int s
   __shared__ __attribute__((aligned(16))) f32x4 part[2][kNW][kTN][64];
   const int ntile = (g.nout + kCols - 1) / kCols;
   int e, row0, nrows, ct;
-  if (!find_tile(g.offsets, g.E, g.M, 16, (ntile + span - 1) / span, e, row0, nrows, ct)) return;
+  if (!find_tile(g, 16, (ntile + span - 1) / span, e, row0, nrows, ct)) return;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l16 = lane & 15, grp = lane >> 4;
   const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
