@@ -100,6 +100,14 @@ __device__ __forceinline__ void dma16(const char* p, int64_t bytes, uint32_t off
   }
 }
 
+// The wait states between an MFMA and the first other use of its result, by
+// hand: where that use stands behind a branch, the compiler has been seen to
+// leave them out (and the use to read the sums of two MFMAs before).
+template <typename V>
+__device__ __forceinline__ void mfma_done(V& acc) {
+  asm volatile("s_nop 15\n\ts_nop 3" : "+v"(acc));
+}
+
 // One operand's side of a tile: kC rows (contraction-contiguous, !kT) or
 // columns (output-contiguous, kT), staged by kNW waves.
 template <bool kT, int kC, int kNW>
@@ -375,6 +383,7 @@ struct Tile {
     for (; ks < nks; ++ks) step(std::integral_constant<int, 0>{}, ks);
     __builtin_amdgcn_s_waitcnt(0);   // copies of steps past the end
     __syncthreads();
+    mfma_done(acc[kTN - 1][kTM - 1]);   // (the last one's; the barrier stands behind them all)
   }
 
   // The same for a contraction of one step at most (bf16, one buffer each):
@@ -408,6 +417,7 @@ struct Tile {
                                                               __builtin_bit_cast(bf16x8, fb[m]), acc[n][m], 0, 0, 0);
     }
     __syncthreads();
+    mfma_done(acc[kTN - 1][kTM - 1]);
   }
 
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
@@ -730,19 +740,20 @@ __global__ __launch_bounds__(256) void sum_segments_kernel(GroupedArgs g) {
 
 // ---------------------------------------------------------------------------
 // Few rows per expert (decode): the product streams the weights once and the
-// matrix cores have time to spare, so a workgroup takes at most 16 rows of an
-// expert and 16 kTN columns, and its waves split the contraction.  A wave
-// reads units of 256 B of its weight rows straight into MFMA operands
-// (16x16x32 bf16 / 16x16x128 MXFP4), one unit ahead, lane group g = lane / 16
-// holding chunk 4 j + g of the unit for MFMA j, so that 64 consecutive bytes
-// of 16 rows are read at a time.  The waves' sums are added in wave order
-// through LDS.
+// matrix cores have time to spare, so a work item is at most 16 rows of an
+// expert by 16 columns, and belongs to the four waves of a workgroup, which
+// split the contraction and add their sums in wave order through LDS (kSplit),
+// or to one wave.  A wave reads units of 256 B of its weight rows straight
+// into MFMA operands (16x16x32 bf16 / 16x16x128 MXFP4), one unit ahead, lane
+// group g = lane / 16 holding chunk 4 j + g of the unit for MFMA j, so that 64
+// consecutive bytes of 16 rows are read at a time.  Bound by HBM: 5.2 TB/s for
+// two rows over eight experts of N = 28672, K = 4096, 5.5 TB/s for 256 rows
+// over 64 experts of N = K = 2048 (bf16).
 // ---------------------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnitBytes = 256;
-constexpr int kFewRowsGroups = 2048;
 
 // Sixteen scale bytes of a row: those of unit u, zeros past the row's end
 // (where the last sixteen of the row are read and shifted down).
@@ -768,125 +779,106 @@ __device__ __forceinline__ u32x4 unit_scales(const uint8_t* p, int n, int u) {
   return u32x4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1], (uint32_t)(v[1] >> 32)};
 }
 
-template <bool kMX, int kTN, int kNW>
-__global__ __launch_bounds__(64 * kNW) void few_rows_kernel(GroupedArgs g, int span) {
-  constexpr int kCols = 16 * kTN;
-  __shared__ __attribute__((aligned(16))) f32x4 part[2][kNW][kTN][64];
-  const int ntile = (g.nout + kCols - 1) / kCols;
+constexpr int kFewWaves = 4;
+
+template <bool kMX, bool kSplit>
+__global__ __launch_bounds__(64 * kFewWaves) void few_rows_kernel(GroupedArgs g) {
+  constexpr int kCols = kSplit ? 16 : 16 * kFewWaves;   // of a workgroup
+  __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][64];
   int e, row0, nrows, ct;
-  if (!find_tile(g, 16, (ntile + span - 1) / span, e, row0, nrows, ct)) return;
-  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  if (!find_tile(g, 16, (g.nout + kCols - 1) / kCols, e, row0, nrows, ct)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, grp = lane >> 4;
   const int kbytes = kMX ? g.kc / 2 : 2 * g.kc;
-  const int tile0 = ct * span, tiles = min(span, ntile - tile0);
+  const int c0 = ct * kCols + (kSplit ? 0 : 16 * wave), ncols = min(16, g.nout - c0);
+  if (!kSplit && ncols <= 0) return;   // (no barrier there)
   const __amdgpu_buffer_rsrc_t rx = buffer(static_cast<const char*>(g.x) + (int64_t)row0 * kbytes, (int64_t)nrows * kbytes);
-  const char* wbase = static_cast<const char*>(g.w) + (int64_t)e * g.nout * kbytes;
+  const __amdgpu_buffer_rsrc_t rw =
+      buffer(static_cast<const char*>(g.w) + ((int64_t)e * g.nout + c0) * kbytes, (int64_t)ncols * kbytes);
   const int nscale = g.kc / 32;
-  const uint8_t* xs = nullptr;
-  if constexpr (kMX)
+  const uint8_t *xs = nullptr, *ws = nullptr;
+  if constexpr (kMX) {
     if (l16 < nrows) xs = g.x_scales + (int64_t)(row0 + l16) * nscale;
+    if (l16 < ncols) ws = g.w_scales + ((int64_t)e * g.nout + c0 + l16) * nscale;
+  }
 
   struct Unit {
-    u32x4 w[kTN][4], x[4], sw[kTN], sx;
+    u32x4 w[4], x[4], sw, sx;
   };
-  // step i of this wave: its unit i % steps (of units wave, wave + kNW, ...) of
-  // the workgroup's column tile i / steps; what is out of range loads zeros
-  const int units = (kbytes + kUnitBytes - 1) / kUnitBytes, steps = (units + kNW - 1) / kNW;
-  auto load = [&](Unit& v, int tile, int step) {
-    const int u = step * kNW + wave, c0 = (tile0 + tile) * kCols, ncols = min(kCols, g.nout - c0);
-    const __amdgpu_buffer_rsrc_t rw = buffer(wbase + (int64_t)c0 * kbytes, (int64_t)ncols * kbytes);
+  // unit u (what is out of range loads zeros)
+  auto load = [&](Unit& v, int u) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = u * kUnitBytes + 64 * j + 16 * grp;
-      const bool in = at < kbytes;
-#pragma unroll
-      for (int n = 0; n < kTN; ++n)
-        v.w[n][j] = buffer_load16(rw, in ? (uint32_t)(16 * n + l16) * (uint32_t)kbytes + (uint32_t)at : kPast);
-      v.x[j] = buffer_load16(rx, in ? (uint32_t)l16 * (uint32_t)kbytes + (uint32_t)at : kPast);
+      const uint32_t off = at < kbytes ? (uint32_t)l16 * (uint32_t)kbytes + (uint32_t)at : kPast;
+      v.w[j] = buffer_load16(rw, off);
+      v.x[j] = buffer_load16(rx, off);
     }
     if constexpr (kMX) {
       v.sx = unit_scales(xs, nscale, u);
-      const uint8_t* ws = g.w_scales + ((int64_t)e * g.nout + c0 + l16) * nscale;
-#pragma unroll
-      for (int n = 0; n < kTN; ++n)
-        v.sw[n] = unit_scales(16 * n + l16 < ncols ? ws + (int64_t)16 * n * nscale : nullptr, nscale, u);
+      v.sw = unit_scales(ws, nscale, u);
     }
   };
-  f32x4 acc[kTN];
-#pragma unroll
-  for (int n = 0; n < kTN; ++n) acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   auto use = [&](const Unit& v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int n = 0; n < kTN; ++n) {
-        if constexpr (kMX) {
-          const u32x4 a = v.w[n][j], b = v.x[j];
-          const i32x8 xa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-          const i32x8 xb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-          acc[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, xb, acc[n], 4, 4, 0, v.sw[n][j] >> (8 * grp), 0,
-                                                                    v.sx[j] >> (8 * grp));
-        } else {
-          acc[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.w[n][j]),
-                                                           __builtin_bit_cast(bf16x8, v.x[j]), acc[n], 0, 0, 0);
-        }
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (kMX) {
+        const u32x4 a = v.w[j], b = v.x[j];
+        const i32x8 xa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+        const i32x8 xb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(xa, xb, acc, 4, 4, 0, v.sw[j] >> (8 * grp), 0,
+                                                               v.sx[j] >> (8 * grp));
+      } else {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.w[j]),
+                                                      __builtin_bit_cast(bf16x8, v.x[j]), acc, 0, 0, 0);
       }
-  };
-  // The sums of a finished column tile, and its stores.  Two buffers in turn:
-  // a wave is past the barrier of one tile before it writes the next one's.
-  auto finish = [&](int tile) {
-    auto& p = part[tile & 1];
-#pragma unroll
-    for (int n = 0; n < kTN; ++n) {
-      p[wave][n][lane] = acc[n];
-      acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    // (an LDS barrier: the next unit's loads stay in flight)
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    const int c0 = (tile0 + tile) * kCols;
-    // lane l of block n holds columns 16 n + 4 (l / 16) .. +3 of row l % 16
-    for (int i = t; i < kTN * 64; i += 64 * kNW) {
-      const int n = i >> 6, l = i & 63, c = c0 + 16 * n + 4 * (l >> 4), r = l & 15;
-      f32x4 s = p[0][n][l];
-#pragma unroll
-      for (int v = 1; v < kNW; ++v) {
-        const f32x4 q = p[v][n][l];
-        s.x += q.x; s.y += q.y; s.z += q.z; s.w += q.w;
-      }
-      if (r < nrows && c < g.nout)
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + r) * g.nout + c) =
-            make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-    }
+    mfma_done(acc);
   };
+  const int units = (kbytes + kUnitBytes - 1) / kUnitBytes;
+  constexpr int kStep = kSplit ? kFewWaves : 1;
   Unit va, vb;
-  int tile = 0, step = 0;   // of the unit in use
-  const int total = tiles * steps;
-  auto advance = [&](Unit& cur, Unit& nxt, int i) {
-    const bool last = step + 1 == steps;
-    if (i + 1 < total) load(nxt, last ? tile + 1 : tile, last ? 0 : step + 1);
-    use(cur);
-    if (last) finish(tile);
-    tile += last ? 1 : 0;
-    step = last ? 0 : step + 1;
-  };
-  load(va, 0, 0);
-  for (int i = 0; i < total; i += 2) {
-    advance(va, vb, i);
-    if (i + 1 < total) advance(vb, va, i + 1);
+  int u = kSplit ? wave : 0;
+  if (u < units) load(va, u);
+  while (u < units) {
+    if (u + kStep < units) load(vb, u + kStep);
+    use(va);
+    u += kStep;
+    if (u >= units) break;
+    if (u + kStep < units) load(va, u + kStep);
+    use(vb);
+    u += kStep;
   }
+  if constexpr (kSplit) {
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) {
+      const f32x4 q = part[v][lane];
+      acc.x += q.x; acc.y += q.y; acc.z += q.z; acc.w += q.w;
+    }
+  }
+  // the lane holds columns 4 (lane / 16) .. +3 of row lane % 16
+  if (l16 < nrows && 4 * grp < ncols)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + l16) * g.nout + c0 + 4 * grp) =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
-template <bool kMX, int kTN, int kNW>
+template <bool kMX>
 hipError_t launch_few_rows(const GroupedArgs& g, hipStream_t s) {
-  const int64_t ntile = (g.nout + 16 * kTN - 1) / (16 * kTN);
-  const int64_t slots = (int64_t)g.M / 16 + (g.E < g.M ? g.E : g.M);
-  // column tiles a workgroup takes in turn: enough workgroups to fill the
-  // card a few times over, so that its prefetch runs on from tile to tile
-  const int64_t span = std::max<int64_t>(1, std::min<int64_t>(ntile, slots * ntile / kFewRowsGroups));
-  const int64_t grid = items_grid(slots * ((ntile + span - 1) / span));
-  few_rows_kernel<kMX, kTN, kNW><<<(unsigned)grid, 64 * kNW, 0, s>>>(g, (int)span);
+  const int64_t tiles = (g.nout + 15) / 16, slots = (int64_t)g.M / 16 + (g.E < g.M ? g.E : g.M);
+  // Long rows are split over the waves (bf16, K = 2048, 512 rows over 128
+  // experts: 143 us, 154 whole); rows of less than two units a wave are not,
+  // where there are tiles enough for every wave to have its own (MXFP4, K =
+  // 2880, 64 rows over 32 experts: 60 us, 73 split).
+  const int64_t units = ((kMX ? g.kc / 2 : 2 * g.kc) + kUnitBytes - 1) / kUnitBytes;
+  if (units >= 2 * kFewWaves || slots * tiles < 4096)
+    few_rows_kernel<kMX, true><<<(unsigned)items_grid(slots * tiles), 64 * kFewWaves, 0, s>>>(g);
+  else
+    few_rows_kernel<kMX, false>
+        <<<(unsigned)items_grid(slots * ((tiles + kFewWaves - 1) / kFewWaves)), 64 * kFewWaves, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -922,7 +914,7 @@ bool few_tiles(const GroupedArgs& g) {
 
 template <bool kMX>
 hipError_t launch_forward(const GroupedArgs& g, hipStream_t s) {
-  if (streams(g)) return launch_few_rows<kMX, 1, 4>(g, s);
+  if (streams(g)) return launch_few_rows<kMX>(g, s);
   if constexpr (!kMX)
     if (g.kc <= 64) return launch_rows<false, false, 4, 1, 1, 2, 1, 1>(g, s);
   if (few_tiles(g)) return launch_rows<kMX, false, 4, 2, 1, 4, 3, 3>(g, s);
