@@ -901,9 +901,14 @@ hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Whether the product does little more than stream one operand past the other:
-// few rows per expert (the weights), or few output columns (the rows).
-bool streams(const GroupedArgs& g) { return g.M <= 16 * g.E || g.nout <= 32; }
+// Whether the product does little more than stream one operand past the
+// other, row by row or column by column: few rows per expert (the weights;
+// bf16, E = 64, N = K = 2048: 8 rows an expert 109 us, 125 in tiles, 16 rows
+// 155 and 125; MXFP4, half the bytes and as many loads of scales: two rows, E =
+// 32, N = 5760, K = 2880, 58 and 70 us, four, E = 8, N = K = 4096, 21 and 14),
+// or few output columns (the rows; E = 64, 64 rows, N = 16, K = 2048: 11 us, 17
+// in tiles, N = 32 with 512 rows 64 and 39).
+bool streams(const GroupedArgs& g, bool mx) { return g.M <= (mx ? 2 : 8) * g.E || g.nout <= 16; }
 
 // Whether tiles of 256 x 256 would leave compute units without work; those of
 // half the columns then do better (and have room for a third buffer).
@@ -914,7 +919,7 @@ bool few_tiles(const GroupedArgs& g) {
 
 template <bool kMX>
 hipError_t launch_forward(const GroupedArgs& g, hipStream_t s) {
-  if (streams(g)) return launch_few_rows<kMX>(g, s);
+  if (streams(g, kMX)) return launch_few_rows<kMX>(g, s);
   if constexpr (!kMX)
     if (g.kc <= 64) return launch_rows<false, false, 4, 1, 1, 2, 1, 1>(g, s);
   if (few_tiles(g)) return launch_rows<kMX, false, 4, 2, 1, 4, 3, 3>(g, s);
