@@ -496,6 +496,8 @@ def moeq_dequantize(q, out=None, stream=None):
         if made:
             out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         qc = q._desc()
+        if out.numel() == 0:
+            return out
         with _current(dev):
             _check(_load().moeq_dequantize_mxfp4(ctypes.byref(qc), _ptr(out), _stream(stream, dev)),
                    "moeq_dequantize_mxfp4")

@@ -2,7 +2,6 @@
 // clipping: host-side validation and dispatch.  As in api.hip, every check
 // runs before the first HIP call, so a rejected call has no side effect.
 #include <algorithm>
-#include <new>
 #include <vector>
 
 #include "grouped.h"
@@ -114,7 +113,7 @@ moeq_status moeq_grouped_mm_grad_input(const uint16_t* dy, const uint16_t* w, co
 
 size_t moeq_grouped_mm_grad_weight_workspace_bytes(int32_t M, int32_t E, int32_t N, int32_t K) {
   if (check_grouped(M, E, N, K) != MOEQ_OK) return 0;
-  return sizeof(float) * (size_t)grad_weight_slots(M, grad_weight_segment(M, E, N, K)) * N * K;
+  return sizeof(float) * (size_t)grad_weight_slots(M, grad_weight_segment(M, N, K)) * N * K;
 }
 
 moeq_status moeq_grouped_mm_grad_weight(const uint16_t* dy, const uint16_t* x, const int32_t* offsets, int32_t M,
@@ -129,7 +128,7 @@ moeq_status moeq_grouped_mm_grad_weight(const uint16_t* dy, const uint16_t* x, c
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOEQ_EWORKSPACE;
   if (need > 0 && !aligned16(workspace)) return MOEQ_EALIGN;
   GroupedArgs g = {x, dy, nullptr, nullptr, offsets, dw, M, E, N, K};
-  g.segment = grad_weight_segment(M, E, N, K);
+  g.segment = grad_weight_segment(M, N, K);
   g.slots = (int32_t)grad_weight_slots(M, g.segment);
   g.partial = static_cast<float*>(workspace);
   return device_status(launch_grouped_mm_grad_weight(g, dtype == MOEQ_DTYPE_FP32, static_cast<hipStream_t>(stream)));
@@ -171,8 +170,8 @@ moeq_status moeq_clip_grad_norm(const moeq_grad* grads, int32_t count, double ma
   if (!aligned16(workspace)) return MOEQ_EALIGN;
   try {
     if (overlapping(grads, count)) return MOEQ_EINVAL;
-  } catch (const std::bad_alloc&) {
-    return MOEQ_EDEVICE;
+  } catch (...) {   // (no room on the host for the ranges)
+    return MOEQ_EWORKSPACE;
   }
   return device_status(launch_clip(grads, count, max_norm, norm, static_cast<double*>(workspace),
                                    static_cast<hipStream_t>(stream)));

@@ -28,7 +28,7 @@ struct GroupedArgs {
   int32_t segment = 0, slots = 0;
   float* partial = nullptr;
 };
-int32_t grad_weight_segment(int32_t M, int32_t E, int32_t N, int32_t K);
+int32_t grad_weight_segment(int32_t M, int32_t N, int32_t K);
 int64_t grad_weight_slots(int32_t M, int32_t segment);   // [N][K] slots of the workspace
 hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s);
 hipError_t launch_grouped_mm_mxfp4(const GroupedArgs& g, hipStream_t s);

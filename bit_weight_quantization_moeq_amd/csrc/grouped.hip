@@ -546,7 +546,8 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int max_rows, in
   const int w = work_item(total, kTileGroup * ncol);
   if (w >= total) return false;
   int before = 0;
-  return x.visit([&](int i, int lo, int n) {
+  nrows = 0;
+  x.visit([&](int i, int lo, int n) {
     const int nt = (n + max_rows - 1) / max_rows, incl = wave_scan(nt);
     const int first = before + incl - nt;
     const uint64_t hit = __ballot(w >= first * ncol && w < (first + nt) * ncol);
@@ -560,11 +561,13 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int max_rows, in
     const int rr = r - grp * kTileGroup * ncol;
     ct = rr / gt;
     const int mt = grp * kTileGroup + (rr - ct * gt);
+    if (mt >= k) return true;   // (only offsets that do not ascend come here)
     const int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
     row0 = r0 + a;
     nrows = b - a;
     return true;
   });
+  return nrows > 0;
 }
 
 // forward (kAT = false, kMX or not) and grad_input (kAT = true).
@@ -956,7 +959,7 @@ hipError_t launch_weight_for(const GroupedArgs& g, hipStream_t s) {
     case WeightTile::kFewCols: e = launch_weight<Out, 2, 2, 1, 4, 2, 2>(g, s); break;
     default: e = launch_weight<Out, 4, 2, 2, 4, 3, 2>(g, s);
   }
-  const int32_t many = g.M / g.segment;   // experts of more than one segment, at most
+  const int32_t many = g.M / (g.segment + 1);   // experts of more than one segment, at most
   if (e != hipSuccess || many == 0) return e;
   const int64_t blocks = ((int64_t)g.nout * g.kc / 4 + 255) / 256;
   sum_segments_kernel<Out><<<dim3((unsigned)std::min<int64_t>(blocks, 1024), (unsigned)many), 256, 0, s>>>(g);
@@ -965,11 +968,10 @@ hipError_t launch_weight_for(const GroupedArgs& g, hipStream_t s) {
 
 }  // namespace
 
-int32_t grad_weight_segment(int32_t M, int32_t E, int32_t N, int32_t K) {
+int32_t grad_weight_segment(int32_t M, int32_t N, int32_t K) {
   // Enough segments to fill the card when every expert had one (1024 narrow
   // or 256 square tiles), of at least 512 rows: eight steps, so that a slot's
   // traffic stays below that of the rows.
-  (void)E;
   const WeightTile w = weight_tile(N, K);
   const int64_t rows = w == WeightTile::kFewRows ? 64 : 256, cols = w == WeightTile::kFewRows ? 128 : w == WeightTile::kFewCols ? 64 : 256;
   const int64_t tiles = ((N + rows - 1) / rows) * ((K + cols - 1) / cols);
@@ -978,7 +980,10 @@ int32_t grad_weight_segment(int32_t M, int32_t E, int32_t N, int32_t K) {
   return (int32_t)((len + 63) / 64 * 64);
 }
 
-int64_t grad_weight_slots(int32_t M, int32_t segment) { return 2 * (int64_t)(M / segment); }
+int64_t grad_weight_slots(int32_t M, int32_t segment) {
+  const int64_t many = M / (segment + 1);   // experts of more than one segment, each with at most one not full
+  return many ? M / segment + many : 0;
+}
 
 hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool fp32, hipStream_t s) {
   return fp32 ? launch_weight_for<float>(g, s) : launch_weight_for<uint16_t>(g, s);

@@ -310,3 +310,41 @@ def test_mxfp4_layer_matches_its_dequantized_weights():
     mag = grouped_mm(np.abs(_f64(xd)), np.abs(_f64(wd)), host(off))
     # the same exact products: two fp32 sums of 288 terms, two roundings
     assert (np.abs(a - b) <= 2.0 ** -7 * np.abs(b) * (1 + 2.0 ** -7) + 2 * 288 * 2.0 ** -23 * mag * (1 + 2.0 ** -7)).all()
+
+
+def test_operands_past_32_bit_offsets():
+    """x, w and the outputs of more than 2^32 bytes: the last rows and the last
+    expert against fp64."""
+    say("grouped large")
+    g = torch.Generator(device=DEV).manual_seed(31)
+
+    def check(got, a, b, L):   # got = a @ b^T
+        a, b = a.double(), b.double()
+        want, mag = a @ b.t(), a.abs() @ b.abs().t()
+        assert bool(((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + L * 2.0 ** -23 * mag * (1 + 2.0 ** -8)).all())
+
+    M, N, K, E = (1 << 20) + 77, 16, 2056, 3   # x: 4.3 GB; long experts, narrow output
+    x = torch.randn((M, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    w = torch.randn((E, N, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    off = torch.tensor([0, 1000, M - 300, M], dtype=torch.int32, device=DEV)
+    check(moeq.moeq_grouped_mm(x, w, off)[-300:], x[-300:], w[2], K)
+    dy = torch.randn((M, N), generator=g, device=DEV, dtype=torch.bfloat16)
+    check(moeq.moeq_grouped_mm_grad_input(dy, w, off)[-300:], dy[-300:], w[2].t(), N)
+    dw = moeq.moeq_grouped_mm_grad_weight(dy, x, off)
+    check(dw[2], dy[-300:].t(), x[-300:].t(), 300)
+    xq, wq = moeq.moeq_quantize_mxfp4(torch.randn((M, 8192), generator=g, device=DEV, dtype=torch.bfloat16)), \
+        moeq.moeq_quantize_mxfp4(torch.randn((E, 24, 8192), generator=g, device=DEV, dtype=torch.bfloat16))
+    y = moeq.moeq_grouped_mm_mxfp4(xq, wq, off)      # codes: 4.3 GB
+    tail = moeq.QWeight(moeq.FMT_MXFP4, 1, 300, 8192, xq.qdata[:, -300:].contiguous(), None,
+                        xq.scale_codes[:, -300:].contiguous())
+    check(y[-300:], moeq.moeq_dequantize(tail)[0], moeq.moeq_dequantize(wq)[2], 8192)
+    del x, dy, xq, dw
+    E, N, K = 35, 8192, 8192                          # w: 4.7 GB
+    w = torch.randn((E, N, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    for rows in (3, 70):                              # weight streaming, and tiles
+        off = torch.arange(E + 1, dtype=torch.int32, device=DEV) * rows
+        x = torch.randn((E * rows, K), generator=g, device=DEV, dtype=torch.bfloat16)
+        check(moeq.moeq_grouped_mm(x, w, off)[-rows:], x[-rows:], w[-1], K)
+        check(moeq.moeq_grouped_mm_grad_input(x, w, off)[-rows:], x[-rows:], w[-1].t(), N)
+    dw = moeq.moeq_grouped_mm_grad_weight(x, x, off, dtype=torch.bfloat16)
+    check(dw[-1], x[-70:].t(), x[-70:].t(), 70)

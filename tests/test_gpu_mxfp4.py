@@ -90,4 +90,4 @@ def test_out_buffers_streams_and_empty():
     assert torch.equal(back, moeq.moeq_dequantize(ref))
     assert torch.equal(moeq.moeq_dequantize(ref.expert(1)), back[1:])
     e = moeq.moeq_quantize_mxfp4(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV))
-    assert e.shape == (1, 0, 64)
+    assert e.shape == (1, 0, 64) and moeq.moeq_dequantize(e).shape == (1, 0, 64)
