@@ -237,7 +237,8 @@ struct Tile {
     const int wn = wave % kNWN, wm = wave / kNWN;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
     asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
-    char* sc = smem + kScales;   // MX: kCols then kRows rows of 16 B (two steps) in each of two buffers
+    char* sc = smem + kScales;   // MX: two buffers of two steps, each step kCols then kRows rows of 8 B
+    constexpr int kScaleStep = kScaleBuf / 2;
 
     // instruction i of step ks's copies into ring slot `slot`
     auto dma_a = [&](int ks, int slot, int i) { a.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(slot * A::kBytes)); };
@@ -245,7 +246,9 @@ struct Tile {
       b.template dma<kMX>(ks, i, wave, lds0 + (uint32_t)(kBytesB + slot * B::kBytes));
     };
     auto scale_store = [&](int pair, u32x4 v) {
-      *reinterpret_cast<u32x4*>(sc + (pair & 1) * kScaleBuf + 16 * t) = v;
+      char* p = sc + (pair & 1) * kScaleBuf + 8 * t;
+      *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+      *reinterpret_cast<uint2*>(p + kScaleStep) = make_uint2(v.z, v.w);
     };
     // the MFMA order is column block by column block: operand j of kOps is
     // the j-th that it needs (a 0, the b's, the other a's)
@@ -260,11 +263,11 @@ struct Tile {
     };
     // the dwords of step ks: scales 4 h .. 4 h + 3 of the lane's rows
     auto load_scales = [&](int ks, uint32_t (&sa)[kTN], uint32_t (&sb)[kTM]) {
-      const char* s0 = sc + ((ks >> 1) & 1) * kScaleBuf + 16 * (lane & 31) + 8 * (ks & 1) + 4 * (lane >> 5);
+      const char* s0 = sc + (ks & 3) * kScaleStep + 8 * (lane & 31) + 4 * (lane >> 5);
 #pragma unroll
-      for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 16 * 32 * (kTN * wn + n));
+      for (int n = 0; n < kTN; ++n) sa[n] = *reinterpret_cast<const uint32_t*>(s0 + 8 * 32 * (kTN * wn + n));
 #pragma unroll
-      for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 16 * (kCols + 32 * (kTM * wm + m)));
+      for (int m = 0; m < kTM; ++m) sb[m] = *reinterpret_cast<const uint32_t*>(s0 + 8 * (kCols + 32 * (kTM * wm + m)));
     };
     // The step loop.  The barrier stands before the last MFMA step: by then
     // every wave holds that step's operands in registers, so that the LDS
