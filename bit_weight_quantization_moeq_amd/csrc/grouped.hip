@@ -424,53 +424,51 @@ struct Tile {
   }
 
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
-  // out, ld elements a row, staged through LDS so that the stores write whole
-  // rows (from the accumulator layout one instruction would touch 32 rows),
-  // past the caches, which hold the operands (fp32 grad_weight of E = 64,
-  // N = K = 2048: 409 -> 349 us).
-  // Fp32 tiles go by the rows of one row of waves at a time.
+  // out, ld elements a row.  From the accumulator layout one instruction would
+  // touch 32 rows, so every wave takes its blocks of 32 rows through a piece of
+  // LDS of its own (two in turn, no barrier) and stores 128 or 256 B of a row
+  // at a time, past the caches, which hold the operands.
+  template <typename T>
+  static constexpr int kOutPitch = 32 * kTN * (int)sizeof(T) + 16;
+  static constexpr int kOutBufs = kTM > 1 ? 2 : 1;
   template <typename T>
   __device__ __forceinline__ static void store(char* smem, const f32x16 (&acc)[kTN][kTM], T* out, int64_t ld, int nrows,
                                                int ncols) {
-    constexpr int kPer = 16 / (int)sizeof(T);
-    constexpr int kPasses = sizeof(T) == 4 ? kNWM : 1;
-    constexpr int kPassRows = kRows / kPasses;
-    constexpr int kOutPitch = kCols * (int)sizeof(T) + 16;
-    constexpr int kChunks = kCols / kPer;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    constexpr int kPer = 16 / (int)sizeof(T), kLanes = 32 * kTN / kPer;   // lanes per row
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN, l32 = lane & 31, h = lane >> 5;
+    char* piece = smem + wave * (kOutBufs * 32 * kOutPitch<T>);
+    const int c = 32 * kTN * wn + kPer * (lane % kLanes);
 #pragma unroll
-    for (int pass = 0; pass < kPasses; ++pass) {
-      if (pass) __syncthreads();
-      if (kPasses == 1 || wm == pass) {
+    for (int m = 0; m < kTM; ++m) {
+      const int r0 = 32 * (kTM * wm + m);
+      if (r0 >= nrows) break;
+      char* buf = piece + (m & 1) * (32 * kOutPitch<T>);
 #pragma unroll
-        for (int m = 0; m < kTM; ++m) {
-          const int r = 32 * ((kPasses == 1 ? kTM * wm : 0) + m) + l32;
+      for (int n = 0; n < kTN; ++n)
 #pragma unroll
-          for (int n = 0; n < kTN; ++n)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              char* p = smem + r * kOutPitch + (int)sizeof(T) * (32 * (kTN * wn + n) + 8 * q + 4 * h);
-              const f32x16& v = acc[n][m];
-              if constexpr (sizeof(T) == 4)
-                *reinterpret_cast<float4*>(p) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-              else
-                *reinterpret_cast<uint2*>(p) =
-                    make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
-            }
+        for (int q = 0; q < 4; ++q) {
+          char* p = buf + l32 * kOutPitch<T> + (int)sizeof(T) * (32 * n + 8 * q + 4 * h);
+          const f32x16& v = acc[n][m];
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float4*>(p) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          else
+            *reinterpret_cast<uint2*>(p) =
+                make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
         }
-      }
-      __syncthreads();
-      const int first = pass * kPassRows;
-      for (int c = t; c < kPassRows * kChunks; c += 64 * kNW) {
-        const int r = c / kChunks, k = c % kChunks;
-        if (first + r < nrows && kPer * k < ncols)
-          __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(smem + r * kOutPitch + 16 * k),
-                                      reinterpret_cast<u32x4*>(out + (int64_t)(first + r) * ld + kPer * k));
+      // (a wave's LDS accesses are done in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < kLanes / 2; ++u) {
+        const int r = u * (64 / kLanes) + lane / kLanes;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * kOutPitch<T> + 16 * (lane % kLanes));
+        if (r0 + r < nrows && c < ncols)
+          __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + (int64_t)(r0 + r) * ld + c));
       }
     }
   }
-  static constexpr int out_bytes(int size) { return (size == 4 ? kRows / kNWM : kRows) * (kCols * size + 16); }
+  static constexpr int out_bytes(int size) { return kNW * kOutBufs * 32 * (32 * kTN * size + 16); }
 };
 
 constexpr int imax(int a, int b) { return a > b ? a : b; }
