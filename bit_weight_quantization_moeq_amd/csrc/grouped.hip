@@ -35,6 +35,13 @@
 //
 // offsets are data on the device: they are clamped to [0, M] and no tile
 // leaves the arrays whatever they hold.
+//
+// Measured, E = 8 with 4096 rows each, N = K = 4096: bf16 840-870 us (1.26-1.31
+// PFLOP/s; the matrix cores are 77 % busy at the 1.42 GHz that the power
+// leaves), MXFP4 283-295 us (3.7-3.9 PFLOP/s; 50 % busy at 1.76 GHz: a step's
+// copies take two thirds of it, and a tile's first copies and its stores
+// overlap with nothing).  256 x 256 tiles, because their operands are read
+// from L2 least often, with LDS for one workgroup per compute unit.
 #include <algorithm>
 #include <type_traits>
 

@@ -20,7 +20,8 @@
 // its largest magnitude comes from integer maxima (the order of magnitudes is
 // that of their bit patterns) and two DPP steps, and v_cvt_scalef32_pk_*
 // round two values an instruction.  Since a block never straddles a row, a
-// tensor is a flat array of blocks.
+// tensor is a flat array of blocks.  [32, 5760, 2880]: quantize 229 us (5.9
+// TB/s of 2.53 B a value), dequantize 268 us (5.0 TB/s).
 #include "moeq_internal.h"
 
 namespace moeq {
