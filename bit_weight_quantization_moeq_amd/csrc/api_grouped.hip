@@ -35,8 +35,11 @@ moeq_status check_grouped(int32_t M, int32_t E, int32_t N, int32_t K) {
   if (E > MOEQ_MAX_EXPERTS || N > kMaxDim || K > kMaxDim || M > kMaxRows) return MOEQ_ESHAPE;
   if (N % 8 != 0 || K % 8 != 0) return MOEQ_ESHAPE;
   if ((int64_t)N * K * 2 >= kMaxExpertBytes) return MOEQ_ESHAPE;
-  // work items (at least 32 rows by 16 columns, and one row tile more per expert) fit 31 bits
-  if (((int64_t)M / 32 + E) * (N / 16 + 1) >= (int64_t(1) << 31)) return MOEQ_ESHAPE;
+  // The tiles' grids (a quarter more workgroups than tiles) hold less than
+  // 2^32 threads: 512 for a tile of 256 x 256, 256 for one of 64 x 128.
+  const int64_t threads = int64_t(1) << 32;
+  if (((int64_t)M / 256 + E) * (N / 256 + 1) * 640 + 8192 >= threads) return MOEQ_ESHAPE;
+  if (K <= 64 && ((int64_t)M / 64 + E) * (N / 128 + 1) * 320 + 8192 >= threads) return MOEQ_ESHAPE;
   return MOEQ_OK;
 }
 

@@ -919,7 +919,11 @@ hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
 // 32, N = 5760, K = 2880, 58 and 70 us, four, E = 8, N = K = 4096, 21 and 14),
 // or few output columns (the rows; E = 64, 64 rows, N = 16, K = 2048: 11 us, 17
 // in tiles, N = 32 with 512 rows 64 and 39).
-bool streams(const GroupedArgs& g, bool mx) { return g.M <= (mx ? 2 : 8) * g.E || g.nout <= 16; }
+// A grid holds less than 2^32 threads; beyond that the tiles serve.
+bool streams(const GroupedArgs& g, bool mx) {
+  const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
+  return (g.M <= (mx ? 2 : 8) * g.E || g.nout <= 16) && items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
+}
 
 // Whether tiles of 256 x 256 would leave compute units without work; those of
 // half the columns then do better (and have room for a third buffer).

@@ -463,8 +463,10 @@ moeq_status moeq_dequantize_mxfp4(const moeq_qweight *src, uint16_t *out_bf16, v
  * [0, M]; ones that do not ascend give undefined results, but no access
  * outside the arrays.  Every pointer 16-byte aligned, except offsets.
  * MOEQ_ESHAPE unless N and K are multiples of 8 of at most 2^20, N*K*2 < 2^31,
- * E <= MOEQ_MAX_EXPERTS and M <= 2^28.  M == 0 is a valid no-op, except that
- * moeq_grouped_mm_grad_weight then writes zeros.
+ * E <= MOEQ_MAX_EXPERTS, M <= 2^28 and the tiles fit one launch:
+ * (M/256 + E)(N/256 + 1) < 6.7e6, and for K <= 64 (M/64 + E)(N/128 + 1) <
+ * 1.3e7 (N and K exchanged for the input gradient).  M == 0 is a valid no-op,
+ * except that moeq_grouped_mm_grad_weight then writes zeros.
  */
 moeq_status moeq_grouped_mm(const uint16_t *x_bf16, const uint16_t *w_bf16, const int32_t *offsets, int32_t M,
                             int32_t E, int32_t N, int32_t K, uint16_t *out_bf16, void *stream);
