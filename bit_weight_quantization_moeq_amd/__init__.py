@@ -187,12 +187,16 @@ def _current(dev):
     return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here (on the current stream) that a call on ``stream`` uses
-    keep their memory until that work is done."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _empty(shape, dtype, dev, stream):
+    """A new tensor for a call on ``stream`` (None: the current one): from that
+    stream's memory, which nothing queued elsewhere can still be using, and
+    kept until what is queued on the current stream has used it, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _match_qweight(q, shape, formats, name):
@@ -473,13 +477,15 @@ def moeq_quantize_mxfp4(w, out=None, stream=None):
         _match_qweight(out, shape, (FMT_MXFP4,), "out")
         out.validate_layout()
     dev = _on_device("moeq_quantize_mxfp4", w, *(out._tensors() if out is not None else []))
-    q = out if out is not None else QWeight.empty(FMT_MXFP4, *shape, device=dev)
+    q = out
+    if out is None:
+        E, R, C = shape
+        q = QWeight(FMT_MXFP4, E, R, C, _empty((E, R, C // 2), torch.uint8, dev, stream), None,
+                    _empty((E, R, C // MXFP4_BLOCKSIZE), torch.uint8, dev, stream))
     if w.numel():
         qc = q._desc()
         with _current(dev):
             _check(_load().moeq_quantize_mxfp4(_ptr(w), ctypes.byref(qc), _stream(stream, dev)), "moeq_quantize_mxfp4")
-    if out is None:
-        _used_on(stream, *q._tensors())
     return q
 
 
@@ -492,17 +498,14 @@ def moeq_dequantize(q, out=None, stream=None):
         _dev(out, torch.bfloat16, "out", q.shape)
     dev = _on_device("moeq_dequantize", *q._tensors(), out)
     if q.format == FMT_MXFP4:
-        made = out is None
-        if made:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        if out is None:
+            out = _empty(q.shape, torch.bfloat16, dev, stream)
         qc = q._desc()
         if out.numel() == 0:
             return out
         with _current(dev):
             _check(_load().moeq_dequantize_mxfp4(ctypes.byref(qc), _ptr(out), _stream(stream, dev)),
                    "moeq_dequantize_mxfp4")
-        if made:
-            _used_on(stream, out)
         return out
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.qdata.device)
@@ -855,12 +858,10 @@ def moeq_grouped_mm(x, w, offsets, out=None, stream=None):
     if out is not None:
         _dev(out, torch.bfloat16, "out", (M, N))
     dev = _on_device("moeq_grouped_mm", x, w, offsets, out)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
+    y = _empty((M, N), torch.bfloat16, dev, stream) if out is None else out
     with _current(dev):
         _check(_load().moeq_grouped_mm(_ptr(x), _ptr(w), _ptr(offsets), M, E, N, K, _ptr(y), _stream(stream, dev)),
                "moeq_grouped_mm")
-    if out is None:
-        _used_on(stream, y)
     return y
 
 
@@ -873,12 +874,10 @@ def moeq_grouped_mm_grad_input(grad_out, w, offsets, grad_x=None, stream=None):
     if grad_x is not None:
         _dev(grad_x, torch.bfloat16, "grad_x", (M, K))
     dev = _on_device("moeq_grouped_mm_grad_input", grad_out, w, offsets, grad_x)
-    dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev) if grad_x is None else grad_x
+    dx = _empty((M, K), torch.bfloat16, dev, stream) if grad_x is None else grad_x
     with _current(dev):
         _check(_load().moeq_grouped_mm_grad_input(_ptr(grad_out), _ptr(w), _ptr(offsets), M, E, N, K, _ptr(dx),
                                                   _stream(stream, dev)), "moeq_grouped_mm_grad_input")
-    if grad_x is None:
-        _used_on(stream, dx)
     return dx
 
 
@@ -909,18 +908,18 @@ def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_
     if dtype not in _GRAD_DTYPES:
         raise TypeError(f"grad_w must be torch.float32 or torch.bfloat16, got {dtype}")
     dev = _on_device("moeq_grouped_mm_grad_weight", grad_out, x, offsets, grad_w)
-    dw = torch.empty((E, N, K), dtype=dtype, device=dev) if grad_w is None else grad_w
+    dw = _empty((E, N, K), dtype, dev, stream) if grad_w is None else grad_w
     lib = _load()
     need = int(lib.moeq_grouped_mm_grad_weight_workspace_bytes(int(M), int(E), int(N), int(K)))
-    made = workspace is None and need > 0
-    if made or workspace is not None:
+    if workspace is not None:
         workspace = _workspace(workspace, need, dev)
+    elif need > 0:
+        workspace = _empty((need,), torch.uint8, dev, stream)
     with _current(dev):
         _check(lib.moeq_grouped_mm_grad_weight(_ptr(grad_out), _ptr(x), _ptr(offsets), int(M), int(E), int(N), int(K),
                                                _GRAD_DTYPES[dtype], _ptr(dw), _ptr(workspace),
                                                workspace.numel() if workspace is not None else 0, _stream(stream, dev)),
                "moeq_grouped_mm_grad_weight")
-    _used_on(stream, *([dw] if grad_w is None else []), *([workspace] if made else []))
     return dw
 
 
@@ -944,14 +943,12 @@ def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
     if out is not None:
         _dev(out, torch.bfloat16, "out", (M, N))
     dev = _on_device("moeq_grouped_mm_mxfp4", *x._tensors(), *w._tensors(), offsets, out)
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
+    y = _empty((M, N), torch.bfloat16, dev, stream) if out is None else out
     if M:
         xc, wc = x._desc(), w._desc()
         with _current(dev):
             _check(_load().moeq_grouped_mm_mxfp4(ctypes.byref(xc), ctypes.byref(wc), _ptr(offsets), _ptr(y),
                                                  _stream(stream, dev)), "moeq_grouped_mm_mxfp4")
-        if out is None:
-            _used_on(stream, y)
     return y
 
 
@@ -1011,12 +1008,11 @@ def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
     for row in zip(map(_T.data_ptr, grads), map(_T.data_ptr, outs), map(_T.numel, grads),
                    [_GRAD_DTYPES[g.dtype] for g in grads]):
         table.extend(row)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
+    norm = _empty((), torch.float32, dev, stream)
     lib = _load()
-    made = workspace is None
-    workspace = _workspace(workspace, int(lib.moeq_clip_grad_norm_workspace_bytes(len(grads))), dev)
+    need = int(lib.moeq_clip_grad_norm_workspace_bytes(len(grads)))
+    workspace = _empty((need,), torch.uint8, dev, stream) if workspace is None else _workspace(workspace, need, dev)
     with _current(dev):
         _check(lib.moeq_clip_grad_norm(table.buffer_info()[0], len(grads), float(max_norm), _ptr(norm), _ptr(workspace),
                                        workspace.numel(), _stream(stream, dev)), "moeq_clip_grad_norm")
-    _used_on(stream, norm, *([workspace] if made else []))
     return norm

@@ -243,6 +243,34 @@ def test_same_bits_and_streams():
         assert all(torch.equal(a, b) for a, b in zip(ref, out))
 
 
+def test_a_call_on_another_stream_does_not_take_memory_in_use():
+    """Outputs and workspaces of a call on a side stream come from memory that
+    work still queued on the current stream cannot be writing."""
+    say("grouped side stream memory")
+    g = torch.Generator(device=DEV).manual_seed(17)
+    off = torch.tensor([0, 700, 1500], dtype=torch.int32, device=DEV)
+    x = torch.randn((1500, 512), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randn((2, 256, 512), generator=g, device=DEV).to(torch.bfloat16)
+    dy = torch.randn((1500, 256), generator=g, device=DEV).to(torch.bfloat16)
+    ref = [moeq.moeq_grouped_mm(x, w, off), moeq.moeq_grouped_mm_grad_weight(dy, x, off),
+           moeq.moeq_dequantize(moeq.moeq_quantize_mxfp4(x))]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    big = torch.zeros((1 << 28,), device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(6):
+        big.add_(1.0)                                 # keeps the current stream busy (milliseconds)
+    late = [torch.empty_like(t) for t in ref]         # written behind that, freed at once
+    for t in late:
+        t.fill_(5.0)
+    del late, t
+    q = moeq.moeq_quantize_mxfp4(x, stream=side)
+    got = [moeq.moeq_grouped_mm(x, w, off, stream=side), moeq.moeq_grouped_mm_grad_weight(dy, x, off, stream=side),
+           moeq.moeq_dequantize(q, stream=side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
 def test_captured_and_replayed():
     say("grouped graph")
     x, w, dy, off, doff = _case("empty experts", 72, 160)
