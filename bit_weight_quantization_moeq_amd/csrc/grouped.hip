@@ -13,7 +13,7 @@
 // columns are the MFMA A operand (so a lane ends up with four consecutive
 // output columns of one row) and its rows the B operand.  Each contraction
 // step takes 128 bytes of contraction of every tile row and column through
-// LDS, double-buffered, copied by the LDS DMA of buffer_load ... lds:
+// LDS, in two or three buffers, copied by the LDS DMA of buffer_load ... lds:
 //   * an operand that is contiguous along the contraction (x, w and dy of the
 //     first two products) lies in LDS as rows of 128 B whose 16-B slots are
 //     XOR-swizzled by the row, and is read with ds_read_b128;
@@ -399,7 +399,8 @@ struct Tile {
   // The same for a contraction of one step at most (bf16, one buffer each):
   // the product moves its output and little else, so the tile is kept small
   // enough for four workgroups per compute unit, whose copies, products and
-  // stores overlap.
+  // stores overlap (E = 64, 512 rows each, N = 2048, K = 64: 27 us, 5.0 TB/s of
+  // output; rank-16 grad_input over 128 experts 12-14 us, 27 in tiles of 128 rows).
   __device__ __forceinline__ static void run_short(char* smem, const A& a, const B& b, int kbytes, f32x16 (&acc)[kTN][kTM]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN;
@@ -433,7 +434,7 @@ struct Tile {
   // Stores the tile: rows r < nrows, columns c < ncols (a multiple of 8) of
   // out, ld elements a row.  From the accumulator layout one instruction would
   // touch 32 rows, so every wave takes its blocks of 32 rows through a piece of
-  // LDS of its own (two in turn, no barrier) and stores 128 or 256 B of a row
+  // LDS of its own (two in turn, no barrier) and stores 64 to 256 B of a row
   // at a time, past the caches, which hold the operands.
   template <typename T>
   static constexpr int kOutPitch = 32 * kTN * (int)sizeof(T) + 16;
@@ -530,7 +531,8 @@ struct ExpertRows {
 // go to the XCDs in turn, so that neighbours share an L2, but an expert with
 // many rows does not leave its work to one XCD (contiguous eighths: rank-16
 // grad_weight over Zipf-distributed experts 31 instead of 22 us, square
-// products 3 % slower); at most total / 32, so that every XCD has several.  Needs a grid of at least items_grid(total) workgroups.
+// products 3 % slower); at most total / 32, so that every XCD has several.
+// Needs a grid of at least items_grid(total) workgroups.
 __device__ __forceinline__ int work_item(int total, int run) {
   run = max(min(run, total / (4 * kXcds)), 1);
   const int slot = blockIdx.x / kXcds, q = slot / run;
@@ -926,7 +928,9 @@ bool streams(const GroupedArgs& g, bool mx) {
 }
 
 // Whether tiles of 256 x 256 would leave compute units without work; those of
-// half the columns then do better (and have room for a third buffer).
+// half the columns then do better (and have room for a third buffer): bf16, E =
+// 8, 128 rows each, N = 4096, K = 14336 (128 tiles) 191-208 us against 232-270;
+// with 144 tiles (E = 1, 4096 rows, N = 2304, K = 4096) 103 against 78.
 bool few_tiles(const GroupedArgs& g) {
   const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
   return rows * ((g.nout + 255) / 256) <= 128;
