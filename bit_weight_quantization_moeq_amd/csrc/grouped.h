@@ -28,6 +28,17 @@ struct GroupedArgs {
   int32_t segment = 0, slots = 0;
   float* partial = nullptr;
 };
+
+// The rows of an expert between two offsets, which can hold anything: both are
+// clamped to [0, M], and the expert has no rows where they do not ascend.
+struct RowRange {
+  int32_t lo, n;
+};
+__host__ __device__ inline RowRange row_range(int32_t from, int32_t to, int32_t M) {
+  const int32_t lo = from < 0 ? 0 : from < M ? from : M, hi = to < 0 ? 0 : to < M ? to : M;
+  return {lo, hi > lo ? hi - lo : 0};
+}
+
 int32_t grad_weight_segment(int32_t M, int32_t N, int32_t K);
 int64_t grad_weight_slots(int32_t M, int32_t segment);   // [N][K] slots of the workspace
 hipError_t launch_grouped_mm(const GroupedArgs& g, hipStream_t s);

@@ -505,8 +505,9 @@ struct ExpertRows {
   int32_t E, M;
   int lo[kKept], n[kKept];
   __device__ __forceinline__ void rows(int i, int& l, int& c) const {   // none past the last expert
-    l = min(max(offsets[min(i, E)], 0), M);
-    c = max(min(offsets[min(i + 1, E)], M) - l, 0);
+    const RowRange r = row_range(offsets[min(i, E)], offsets[min(i + 1, E)], M);
+    l = r.lo;
+    c = r.n;
   }
   __device__ __forceinline__ ExpertRows(const GroupedArgs& g) : offsets(g.offsets), E(g.E), M(g.M) {
 #pragma unroll
