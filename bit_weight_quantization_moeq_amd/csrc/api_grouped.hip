@@ -18,11 +18,12 @@ constexpr int32_t kMaxDim = 1 << 20;     // N and K of a grouped product
 constexpr int64_t kMaxExpertBytes = int64_t(1) << 31;
 constexpr int32_t kMaxRows = 1 << 28;    // M of a grouped product
 
-moeq_status check_mxfp4(const moeq_qweight* q) {
+// may_be_empty: rows == 0 is allowed, and the data pointers may then be null.
+moeq_status check_mxfp4(const moeq_qweight* q, bool may_be_empty = false) {
   if (!q) return MOEQ_EINVAL;
   if (q->format != MOEQ_FMT_MXFP4) return MOEQ_EFORMAT;
-  if (q->num_experts <= 0 || q->rows <= 0 || q->cols <= 0) return MOEQ_EINVAL;
-  if (!q->qdata || !q->scale_codes || q->scales) return MOEQ_EINVAL;
+  if (q->num_experts <= 0 || q->rows < (may_be_empty ? 0 : 1) || q->cols <= 0) return MOEQ_EINVAL;
+  if ((q->rows > 0 && (!q->qdata || !q->scale_codes)) || q->scales) return MOEQ_EINVAL;
   if (q->blocksize != MOEQ_MXFP4_BLOCKSIZE || q->cols % MOEQ_MXFP4_BLOCKSIZE != 0) return MOEQ_EBLOCK;
   if (!aligned16(q->qdata) || !aligned16(q->scale_codes)) return MOEQ_EALIGN;
   return MOEQ_OK;
@@ -139,12 +140,13 @@ moeq_status moeq_grouped_mm_grad_weight(const uint16_t* dy, const uint16_t* x, c
 
 moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight* x, const moeq_qweight* w, const int32_t* offsets, uint16_t* out,
                                   void* stream) {
-  moeq_status st = check_mxfp4(x);
+  moeq_status st = check_mxfp4(x, true);
   if (st == MOEQ_OK) st = check_mxfp4(w);
   if (st != MOEQ_OK) return st;
   if (x->num_experts != 1 || x->cols != w->cols) return MOEQ_ESHAPE;
   st = check_grouped(x->rows, w->num_experts, w->rows, w->cols);
   if (st != MOEQ_OK) return st;
+  if (x->rows == 0) return MOEQ_OK;
   if (!offsets || !out) return MOEQ_EINVAL;
   if (!aligned16(out)) return MOEQ_EALIGN;
   const GroupedArgs g = {x->qdata, w->qdata, x->scale_codes, w->scale_codes, offsets, out,

@@ -483,7 +483,8 @@ size_t moeq_grouped_mm_grad_weight_workspace_bytes(int32_t M, int32_t E, int32_t
  * ([1][M][K], activations quantized with moeq_quantize_mxfp4), w [E][N][K].
  * The block scales are applied inside the matrix instructions; products are
  * summed in fp32 and rounded once to bf16.  A NaN block makes the outputs
- * that it enters NaN.  Otherwise as moeq_grouped_mm, with K % 32 == 0.
+ * that it enters NaN.  Otherwise as moeq_grouped_mm, with K % 32 == 0; x with
+ * rows == 0 (its data pointers may then be NULL) is a valid no-op.
  */
 moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, const int32_t *offsets,
                                   uint16_t *out_bf16, void *stream);
