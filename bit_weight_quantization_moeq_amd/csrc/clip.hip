@@ -174,41 +174,57 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(Table t, double* __restri
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
+// max_norm / norm as m * 2^e, with e = 0 where fp32 holds the quotient as a
+// normal number.  Below that (large gradients, a small max_norm) fp32 keeps few
+// of its bits or none, but the gradients it scales can come out as normal
+// numbers: the product with m is rounded, and 2^e exact where they do.
+struct Factor {
+  float m;
+  int32_t e;
+  __device__ __forceinline__ static Factor of(double k) {
+    if (!(k < 0x1p-126) || k == 0.0) return {(float)k, 0};
+    int e;
+    const double m = frexp(k, &e);
+    return {(float)m, e};
+  }
+  __device__ __forceinline__ float times(float g) const { return __builtin_ldexpf(g * m, e); }
+};
+
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, float k) {
+__device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, Factor k) {
   each(
       src, n,
       [&](const u32x4& v, int i) {
         float f[Vec<T>::kN];
         Vec<T>::unpack(v, f);
 #pragma unroll
-        for (int j = 0; j < Vec<T>::kN; ++j) f[j] *= k;
+        for (int j = 0; j < Vec<T>::kN; ++j) f[j] = k.times(f[j]);
         const u32x4 o = Vec<T>::pack(f);
         __builtin_nontemporal_store(o, reinterpret_cast<u32x4a*>(dst + (int64_t)i * Vec<T>::kN));
       },
-      [&](int i) { from_float(to_float(src[i]) * k, dst[i]); });
+      [&](int i) { from_float(k.times(to_float(src[i])), dst[i]); });
 }
 
 // The norm and the factor of every gradient: 1 when there is nothing to clip,
 // also for a norm that is no finite number.
 __global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ partial, int32_t partials,
                                                        double max_norm, float* __restrict__ norm_out,
-                                                       float* __restrict__ factor) {
+                                                       Factor* __restrict__ factor) {
   double s = 0.0;
   for (int i = threadIdx.x; i < partials; i += kThreads) s += partial[i];
   const double norm = sqrt(block_sum(s));
   if (threadIdx.x == 0) {
     *norm_out = (float)norm;
-    *factor = norm > max_norm && norm < __builtin_inf() ? (float)(max_norm / norm) : 1.0f;
+    *factor = Factor::of(norm > max_norm && norm < __builtin_inf() ? max_norm / norm : 1.0);
   }
 }
 
-__global__ __launch_bounds__(kThreads) void scale_kernel(Table t, const float* __restrict__ factor) {
+__global__ __launch_bounds__(kThreads) void scale_kernel(Table t, const Factor* __restrict__ factor) {
   // from the back: what the sum read last may still be cached
   const int64_t c = t.chunks - 1 - blockIdx.x;
   const int i = tensor_of(t, c);
-  const float k = *factor;
-  if (k == 1.0f && t.e[i].src == t.e[i].dst) return;  // nothing to change in place
+  const Factor k = *factor;
+  if (k.m == 1.0f && k.e == 0 && t.e[i].src == t.e[i].dst) return;  // nothing to change in place
   const int64_t chunk = chunk_of(is_fp32(t, i)), at = (c - t.e[i].first) * chunk;
   const int n = (int)min(chunk, t.e[i].n - at);
   if (is_fp32(t, i))
@@ -243,7 +259,8 @@ int64_t clip_partials(int32_t count) { return ((int64_t)count + kTable - 1) / kT
 hipError_t launch_clip(const moeq_grad* g, int32_t count, double max_norm, float* norm, double* partial, hipStream_t s) {
   Table t;
   int32_t partials = 0;
-  float* factor = reinterpret_cast<float*>(partial);  // (of the sum over the partials, kept in front of them)
+  static_assert(sizeof(Factor) <= kClipHead * sizeof(double), "the factor lies in front of the partial sums");
+  Factor* factor = reinterpret_cast<Factor*>(partial);
   partial += kClipHead;
   for (int32_t i = 0; i < count;) {
     i = fill(t, g, count, i);
