@@ -984,8 +984,10 @@ def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
     """The norm over all ``grads`` (bf16 and fp32 tensors of any shape) and
     ``grad * min(1, max_norm / norm)``, written in place or into ``out`` (one
     tensor per gradient, of its shape and type).  Returns the norm, an fp32
-    tensor on the device; when it is an infinity or a NaN nothing is scaled.
-    Neither the gradients nor ``out`` may overlap each other."""
+    tensor on the device.  A gradient that is an infinity or a NaN makes the
+    norm one, and nothing is scaled; a norm of finite gradients past fp32's
+    range reads as an infinity, but they are scaled as any others.  Neither
+    the gradients nor ``out`` may overlap each other."""
     grads = list(grads)
     if not grads:
         raise ValueError("grads must hold at least one tensor")

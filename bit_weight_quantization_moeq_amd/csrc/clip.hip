@@ -13,7 +13,8 @@
 //                 leaves the norm and the factor;
 //   scale_kernel  one workgroup per chunk.
 // A square of an fp32 or bf16 value is exact in fp64 and cannot overflow it,
-// so the norm is right to fp32 for every finite gradient.
+// so the norm is right to fp32 for every finite gradient; one past fp32's range
+// is an infinity in the result alone, the factor comes from its fp64 value.
 //
 // Measured, 2.0 GB of fp32 into another buffer: sum 371-383 us (5.3 TB/s), norm
 // 4.6 us, scale 870-900 us (4.5 TB/s, the rate of an elementwise product of
@@ -206,7 +207,7 @@ __device__ __forceinline__ void chunk_scale(const T* src, T* dst, int n, Factor 
 }
 
 // The norm and the factor of every gradient: 1 when there is nothing to clip,
-// also for a norm that is no finite number.
+// also for a norm that is no finite number in fp64 (then some gradient is none).
 __global__ __launch_bounds__(kThreads) void norm_kernel(const double* __restrict__ partial, int32_t partials,
                                                        double max_norm, float* __restrict__ norm_out,
                                                        Factor* __restrict__ factor) {

@@ -498,11 +498,13 @@ moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, 
  * elsewhere must overlap no src and no other dst (MOEQ_EINVAL).  src and dst
  * are aligned to their type.  norm: one fp32 on the device.  The sum is
  * formed in fp64 in a fixed order: the same bits from run to run, and no
- * overflow.  A norm that is an infinity or a NaN scales nothing (dst becomes
- * src), so that the caller can skip the step on *norm alone.  Empty tensors are allowed; count
- * == 0 gives a norm of 0.  MOEQ_EINVAL for a max_norm that is negative or
- * NaN.  Workspace of moeq_clip_grad_norm_workspace_bytes(count), 16-byte
- * aligned.
+ * overflow.  A gradient that is an infinity or a NaN makes the norm one, and
+ * nothing is scaled (dst becomes src).  A norm of finite gradients past fp32's
+ * range reads as an infinity in *norm, but they are scaled by its fp64 value
+ * as any others.  Either way the caller can skip the step on *norm alone.
+ * Empty tensors are allowed; count == 0 gives a norm of 0.  MOEQ_EINVAL for a
+ * max_norm that is negative or NaN.  Workspace of
+ * moeq_clip_grad_norm_workspace_bytes(count), 16-byte aligned.
  */
 typedef struct moeq_grad {
   const void *src;

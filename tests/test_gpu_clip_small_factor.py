@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import bit_weight_quantization_moeq_amd as moeq
-from tests.gpu_common import host, require_native, say
+from tests.gpu_common import DEV, host, require_native, say
 from tests.test_gpu_clip import _check, _grads
 
 pytestmark = pytest.mark.gpu
@@ -33,6 +33,18 @@ def test_factor_near_and_below_fp32_normal_numbers(std, max_norm):
     _check(keep, out, norm, max_norm)
     assert torch.equal(moeq.moeq_clip_grad_norm(grads, max_norm), norm)   # in place
     assert all(torch.equal(a, b) for a, b in zip(grads, out))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_past_fp32_reads_as_an_infinity_and_still_clips(dtype):
+    """64 equal gradients v have the norm 8 v: below, and past, fp32's range."""
+    say(f"clip norm past fp32 {dtype}")
+    for v, finite in ((2.0 ** 124, True), (2.0 ** 125, False), (2.0 ** 127, False)):
+        g = [torch.full((40,), v, dtype=dtype, device=DEV), torch.full((24,), -v, dtype=dtype, device=DEV)]
+        out = [torch.full_like(t, 7.0) for t in g]
+        norm = moeq.moeq_clip_grad_norm(g, 2.0 ** 120, out=out)
+        assert float(norm) == (8 * v if finite else math.inf)
+        assert (out[0] == 2.0 ** 117).all() and (out[1] == -(2.0 ** 117)).all()   # v 2^120 / (8 v)
 
 
 def test_results_below_fp32_normal_numbers():
