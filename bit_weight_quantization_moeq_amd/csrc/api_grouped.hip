@@ -2,6 +2,7 @@
 // clipping: host-side validation and dispatch.  As in api.hip, every check
 // runs before the first HIP call, so a rejected call has no side effect.
 #include <algorithm>
+#include <initializer_list>
 #include <vector>
 
 #include "grouped.h"
@@ -44,15 +45,39 @@ moeq_status check_grouped(int32_t M, int32_t E, int32_t N, int32_t K) {
   return MOEQ_OK;
 }
 
+// Whether what a call writes shares memory with one of the others.  The
+// kernels' workgroups read their operands while others store their results, so
+// such a call would read its own output.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool overlaps(const Span& out, std::initializer_list<Span> others) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(out.p), hi = lo + (uintptr_t)out.bytes;
+  for (const Span& s : others) {
+    const uintptr_t l = reinterpret_cast<uintptr_t>(s.p);
+    if (out.bytes > 0 && s.bytes > 0 && lo < l + (uintptr_t)s.bytes && l < hi) return true;
+  }
+  return false;
+}
+Span bf16(const uint16_t* p, int64_t rows, int64_t cols) { return {p, rows * cols * 2}; }
+Span ints(const int32_t* offsets, int32_t E) { return {offsets, (E + int64_t(1)) * 4}; }
+Span codes(const moeq_qweight* q) { return {q->qdata, blocks(q) * (MOEQ_MXFP4_BLOCKSIZE / 2)}; }
+Span scale_codes(const moeq_qweight* q) { return {q->scale_codes, blocks(q)}; }
+
 // Whether a tensor that is written overlaps any other one (in place, a
-// tensor is one range).
-bool overlapping(const moeq_grad* g, int32_t count) {
+// tensor is one range), or the norm and the workspace.
+bool overlapping(const moeq_grad* g, int32_t count, const Span& norm, const Span& workspace) {
   struct Range {
     uintptr_t lo, hi;
     bool written;
   };
   std::vector<Range> r;
-  r.reserve(2 * (size_t)count);
+  r.reserve(2 * (size_t)count + 2);
+  for (const Span& s : {norm, workspace}) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(s.p);
+    r.push_back({lo, lo + (uintptr_t)s.bytes, true});
+  }
   for (int32_t i = 0; i < count; ++i) {
     if (g[i].numel == 0) continue;
     const uintptr_t size = (uintptr_t)g[i].numel * (g[i].dtype == MOEQ_DTYPE_FP32 ? 4 : 2);
@@ -79,6 +104,8 @@ moeq_status moeq_quantize_mxfp4(const uint16_t* w, const moeq_qweight* dst, void
   if (st != MOEQ_OK) return st;
   if (!w) return MOEQ_EINVAL;
   if (!aligned16(w)) return MOEQ_EALIGN;
+  const Span in = {w, blocks(dst) * 2 * MOEQ_MXFP4_BLOCKSIZE};
+  if (overlaps(codes(dst), {in, scale_codes(dst)}) || overlaps(scale_codes(dst), {in})) return MOEQ_EINVAL;
   return device_status(launch_quantize_mxfp4(w, static_cast<uint8_t*>(dst->qdata), dst->scale_codes, blocks(dst),
                                              static_cast<hipStream_t>(stream)));
 }
@@ -88,6 +115,7 @@ moeq_status moeq_dequantize_mxfp4(const moeq_qweight* src, uint16_t* out, void* 
   if (st != MOEQ_OK) return st;
   if (!out) return MOEQ_EINVAL;
   if (!aligned16(out)) return MOEQ_EALIGN;
+  if (overlaps({out, blocks(src) * 2 * MOEQ_MXFP4_BLOCKSIZE}, {codes(src), scale_codes(src)})) return MOEQ_EINVAL;
   return device_status(launch_dequantize_mxfp4(static_cast<const uint8_t*>(src->qdata), src->scale_codes, out,
                                                blocks(src), static_cast<hipStream_t>(stream)));
 }
@@ -99,6 +127,7 @@ moeq_status moeq_grouped_mm(const uint16_t* x, const uint16_t* w, const int32_t*
   if (M == 0) return MOEQ_OK;
   if (!x || !w || !offsets || !out) return MOEQ_EINVAL;
   if (!aligned16(x) || !aligned16(w) || !aligned16(out)) return MOEQ_EALIGN;
+  if (overlaps(bf16(out, M, N), {bf16(x, M, K), bf16(w, (int64_t)E * N, K), ints(offsets, E)})) return MOEQ_EINVAL;
   const GroupedArgs g = {x, w, nullptr, nullptr, offsets, out, M, E, N, K};
   return device_status(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
 }
@@ -111,6 +140,7 @@ moeq_status moeq_grouped_mm_grad_input(const uint16_t* dy, const uint16_t* w, co
   if (M == 0) return MOEQ_OK;
   if (!dy || !w || !offsets || !dx) return MOEQ_EINVAL;
   if (!aligned16(dy) || !aligned16(w) || !aligned16(dx)) return MOEQ_EALIGN;
+  if (overlaps(bf16(dx, M, K), {bf16(dy, M, N), bf16(w, (int64_t)E * N, K), ints(offsets, E)})) return MOEQ_EINVAL;
   const GroupedArgs g = {dy, w, nullptr, nullptr, offsets, dx, M, E, K, N};
   return device_status(launch_grouped_mm_grad_input(g, static_cast<hipStream_t>(stream)));
 }
@@ -131,6 +161,10 @@ moeq_status moeq_grouped_mm_grad_weight(const uint16_t* dy, const uint16_t* x, c
   const size_t need = moeq_grouped_mm_grad_weight_workspace_bytes(M, E, N, K);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOEQ_EWORKSPACE;
   if (need > 0 && !aligned16(workspace)) return MOEQ_EALIGN;
+  const Span out = {dw, (int64_t)E * N * K * (dtype == MOEQ_DTYPE_FP32 ? 4 : 2)}, sums = {workspace, (int64_t)need};
+  if (overlaps(out, {bf16(dy, M, N), bf16(x, M, K), ints(offsets, E), sums}) ||
+      overlaps(sums, {bf16(dy, M, N), bf16(x, M, K), ints(offsets, E)}))
+    return MOEQ_EINVAL;
   GroupedArgs g = {x, dy, nullptr, nullptr, offsets, dw, M, E, N, K};
   g.segment = grad_weight_segment(M, N, K);
   g.slots = (int32_t)grad_weight_slots(M, g.segment);
@@ -149,6 +183,9 @@ moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight* x, const moeq_qweight* w, 
   if (x->rows == 0) return MOEQ_OK;
   if (!offsets || !out) return MOEQ_EINVAL;
   if (!aligned16(out)) return MOEQ_EALIGN;
+  if (overlaps(bf16(out, x->rows, w->rows),
+               {codes(x), scale_codes(x), codes(w), scale_codes(w), ints(offsets, w->num_experts)}))
+    return MOEQ_EINVAL;
   const GroupedArgs g = {x->qdata, w->qdata, x->scale_codes, w->scale_codes, offsets, out,
                          x->rows, w->num_experts, w->rows, w->cols};
   return device_status(launch_grouped_mm_mxfp4(g, static_cast<hipStream_t>(stream)));
@@ -174,7 +211,9 @@ moeq_status moeq_clip_grad_norm(const moeq_grad* grads, int32_t count, double ma
   if (!workspace || workspace_bytes < moeq_clip_grad_norm_workspace_bytes(count)) return MOEQ_EWORKSPACE;
   if (!aligned16(workspace)) return MOEQ_EALIGN;
   try {
-    if (overlapping(grads, count)) return MOEQ_EINVAL;
+    if (overlapping(grads, count, {norm, sizeof(float)},
+                    {workspace, (int64_t)moeq_clip_grad_norm_workspace_bytes(count)}))
+      return MOEQ_EINVAL;
   } catch (...) {   // (no room on the host for the ranges)
     return MOEQ_EWORKSPACE;
   }

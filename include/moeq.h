@@ -427,7 +427,8 @@ moeq_status moeq_route_buckets(const int32_t *top_k_index, int32_t T, int32_t K,
  * 32 columns: s = max(floor(log2(max |w|)) - 2, -127) + 127, code = the E2M1
  * value nearest to w * 2^(127 - s), ties to the even code, at most 6 in
  * magnitude; an all-zero block stores s = 0 and zero codes.  A block with an
- * infinity or a NaN stores s = 255 (NaN) and zero codes.
+ * infinity or a NaN stores s = 255 (NaN) and zero codes.  MOEQ_EINVAL for
+ * buffers that overlap, here and in moeq_dequantize_mxfp4.
  */
 moeq_status moeq_quantize_mxfp4(const uint16_t *w_bf16, const moeq_qweight *dst, void *stream);
 
@@ -462,6 +463,7 @@ moeq_status moeq_dequantize_mxfp4(const moeq_qweight *src, uint16_t *out_bf16, v
  * reach its results (they may hold anything).  Offsets are clamped to
  * [0, M]; ones that do not ascend give undefined results, but no access
  * outside the arrays.  Every pointer 16-byte aligned, except offsets.
+ * MOEQ_EINVAL for a result that overlaps an operand or the workspace.
  * MOEQ_ESHAPE unless N and K are multiples of 8 of at most 2^20, N*K*2 < 2^31,
  * E <= MOEQ_MAX_EXPERTS, M <= 2^28 and the tiles fit one launch:
  * (M/256 + E)(N/256 + 1) < 6.7e6, and for K <= 64 (M/64 + E)(N/128 + 1) <
@@ -495,8 +497,8 @@ moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, 
  *   dst   = src * min(1, max_norm / *norm), in the tensor's own type
  * grads is a HOST array of `count` descriptors (read before the call
  * returns; src and dst are device memory).  dst == src clips in place; a dst
- * elsewhere must overlap no src and no other dst (MOEQ_EINVAL).  src and dst
- * are aligned to their type.  norm: one fp32 on the device.  The sum is
+ * elsewhere must overlap no src and no other dst, nor any of them norm or the
+ * workspace (MOEQ_EINVAL).  src and dst are aligned to their type.  norm: one fp32 on the device.  The sum is
  * formed in fp64 in a fixed order: the same bits from run to run, and no
  * overflow.  A gradient that is an infinity or a NaN makes the norm one, and
  * nothing is scaled (dst becomes src).  A norm of finite gradients past fp32's
