@@ -24,7 +24,7 @@ def test_grouped_host_code_under_sanitizers(tmp_path):
            "-Xarch_host", "-fno-sanitize-recover=all", "-Xarch_host", "-fno-omit-frame-pointer",
            "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
            "-g", "-O1", "-std=c++17", f"-I{ROOT}/include", f"-I{CSRC}",
-           os.path.join(HERE, "grouped_driver.hip"), "-o", exe]
+           "-w", os.path.join(CSRC, "api_grouped.hip"), os.path.join(HERE, "grouped_driver.hip"), "-o", exe]
     b = subprocess.run(cmd, capture_output=True, text=True)
     assert b.returncode == 0, b.stderr[-4000:]
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=0",
