@@ -191,3 +191,54 @@ def test_more_than_256_experts(name, nout, kc):
     _grad_input(sizes, nout, kc)
     _grad_weight(sizes, nout, kc)
     _mxfp4(sizes, nout, -(-kc // 32) * 32)
+
+
+def _tail(got, want):
+    assert torch.equal(got, want.to(got.dtype))
+
+
+def test_rows_past_32_bit_offsets():
+    """x, the outputs and MXFP4 codes of more than 2^32 bytes, in large tiles:
+    the last rows."""
+    say("grouped exact large rows")
+    g = torch.Generator(device=DEV).manual_seed(11)
+    M, E = (1 << 20) + 77, 3
+    off = torch.tensor([0, 1000, M - 300, M], dtype=torch.int32, device=DEV)
+    for nout, kc in ((264, 2056), (2056, 72)):
+        x, w = _ints8((M, kc), g), _ints8((E, nout, kc), g)
+        _tail(moeq.moeq_grouped_mm(x, w, off)[-700:], torch.cat([x[-700:-300].double() @ w[1].double().t(),
+                                                                x[-300:].double() @ w[2].double().t()]))
+        wt = w.transpose(1, 2).contiguous()
+        _tail(moeq.moeq_grouped_mm_grad_input(x, wt, off)[-300:], x[-300:].double() @ w[2].double().t())
+        del x
+    codes = torch.randint(0, 256, (1, M, 4096), generator=g, device=DEV, dtype=torch.uint8)
+    scales = torch.randint(127, 129, (1, M, 256), generator=g, device=DEV, dtype=torch.uint8)
+    x = moeq.QWeight(moeq.FMT_MXFP4, 1, M, 8192, codes, None, scales)
+    wq, w = _mx((E, 264, 8192), g)
+    y = moeq.moeq_grouped_mm_mxfp4(x, wq, off)
+    values = torch.from_numpy(mxfp4_dequantize(host(codes[0, -300:]), host(scales[0, -300:]))).to(DEV)
+    _tail(y[-300:], values @ w[2].t())
+
+
+def _ints8(shape, g):
+    """As _ints, with less memory on the way."""
+    t = torch.empty(shape, dtype=torch.bfloat16, device=DEV)
+    for s in t.split(max(1, (1 << 28) // t[0].numel())):
+        s.copy_(torch.randint(-8, 9, s.shape, generator=g, device=DEV, dtype=torch.int8))
+    return t
+
+
+@pytest.mark.parametrize("rows", [3, 70, 130, 200, 250])
+def test_weights_past_32_bit_offsets(rows):
+    """w and its gradient of more than 2^32 bytes and long contractions, in the
+    streaming form and tiles of one to four blocks a wave: the last expert."""
+    say(f"grouped exact large weights {rows}")
+    g = torch.Generator(device=DEV).manual_seed(12)
+    E, N, K = 35, 8192, 8192
+    w = _ints8((E, N, K), g)
+    off = torch.arange(E + 1, dtype=torch.int32, device=DEV) * rows
+    x = _ints8((E * rows, K), g)
+    _tail(moeq.moeq_grouped_mm(x, w, off)[-rows:], x[-rows:].double() @ w[-1].double().t())
+    _tail(moeq.moeq_grouped_mm_grad_input(x, w, off)[-rows:], x[-rows:].double() @ w[-1].double())
+    dw = moeq.moeq_grouped_mm_grad_weight(x, x, off, grad_w=w)
+    _tail(dw[-1], x[-rows:].double().t() @ x[-rows:].double())
