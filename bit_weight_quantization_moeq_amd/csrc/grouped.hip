@@ -33,15 +33,16 @@
 // lane holds for the step.  v_mfma_scale_f32_32x32x64_f8f6f4 applies the
 // scales of both operands in the product, with an fp32 sum.
 //
-// offsets are data on the device: they are clamped to [0, M] and no tile
+// offsets are data on the device: row_range clamps them to [0, M], and no tile
 // leaves the arrays whatever they hold.
 //
-// Measured, E = 8 with 4096 rows each, N = K = 4096: bf16 840-870 us (1.26-1.31
-// PFLOP/s; the matrix cores are 77 % busy at the 1.42 GHz that the power
-// leaves), MXFP4 283-295 us (3.7-3.9 PFLOP/s; 50 % busy at 1.76 GHz: a step's
-// copies take two thirds of it, and a tile's first copies and its stores
-// overlap with nothing).  256 x 256 tiles, because their operands are read
-// from L2 least often, with LDS for one workgroup per compute unit.
+// Measured, E = 8 with 4096 rows each, N = K = 4096, call after call: bf16 840-
+// 860 us (1.28-1.31 PFLOP/s), MXFP4 285-325 us (3.4-3.9 PFLOP/s).  Single
+// dispatches under the profiler's counters: bf16 938 us (1.17 PFLOP/s), the
+// matrix cores 77 % busy at 1.46 GHz; MXFP4 306 us (3.6 PFLOP/s), 50 % busy at
+// 1.71 GHz: a step's copies take two thirds of it, and a tile's first copies
+// and its stores overlap with nothing.  256 x 256 tiles, because their operands
+// are read from L2 least often, with LDS for one workgroup per compute unit.
 #include <algorithm>
 #include <type_traits>
 
@@ -399,8 +400,10 @@ struct Tile {
   // The same for a contraction of one step at most (bf16, one buffer each):
   // the product moves its output and little else, so the tile is kept small
   // enough for four workgroups per compute unit, whose copies, products and
-  // stores overlap (E = 64, 512 rows each, N = 2048, K = 64: 27 us, 5.0 TB/s of
-  // output; rank-16 grad_input over 128 experts 12-14 us, 27 in tiles of 128 rows).
+  // stores overlap.  E = 64, 512 rows each, N = 2048, inputs from HBM: K = 16
+  // 29 us and 37 in the large tiles, K = 32 31 and 37, K = 64 43 and 41 (grad_input
+  // alike); K = 72 and 128, which take more than one step, 47-49 in those.
+  // Rank-16 grad_input over 128 experts 11-12 us, 27 in tiles of 128 rows.
   __device__ __forceinline__ static void run_short(char* smem, const A& a, const B& b, int kbytes, f32x16 (&acc)[kTN][kTM]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN;
@@ -916,12 +919,22 @@ hipError_t launch_weight(const GroupedArgs& g, hipStream_t s) {
 }
 
 // Whether the product does little more than stream one operand past the
-// other, row by row or column by column: few rows per expert (the weights;
-// bf16, E = 64, N = K = 2048: 8 rows an expert 109 us, 125 in tiles, 16 rows
-// 155 and 125; MXFP4, half the bytes and as many loads of scales: two rows, E =
-// 32, N = 5760, K = 2880, 58 and 70 us, four, E = 8, N = K = 4096, 21 and 14),
-// or few output columns (the rows; E = 64, 64 rows, N = 16, K = 2048: 11 us, 17
-// in tiles, N = 32 with 512 rows 64 and 39).
+// other, row by row or column by column.  us here and in tiles, inputs from HBM:
+//   few rows per expert (the weights stream)       rows  here  tiles
+//     bf16, E = 64, N = K = 2048                      8   106    123
+//                                                    12   118    125
+//                                                    16   131    124
+//     bf16, E = 8, N = K = 4096                       8    55     61
+//                                                    16    64     61
+//     MXFP4, E = 32, N = 5760, K = 2880            1, 2 65, 66 71, 71
+//                                                  3, 4 67, 68 72, 72
+//     MXFP4, E = 8, N = K = 4096                   1, 2 20, 21 18, 18
+//                                                  3, 4     22     18
+//   few output columns (the rows stream), bf16,       N
+//     E = 64, K = 2048, 64 rows each             16, 32  9, 12 18, 18
+//     512 rows each                              24, 32 58, 61 38, 38
+// so MXFP4, with as many loads of scales for half the bytes, stops at two rows,
+// where the one layer gains as much as the other loses.
 // A grid holds less than 2^32 threads; beyond that the tiles serve.
 bool streams(const GroupedArgs& g, bool mx) {
   const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
@@ -929,9 +942,15 @@ bool streams(const GroupedArgs& g, bool mx) {
 }
 
 // Whether tiles of 256 x 256 would leave compute units without work; those of
-// half the columns then do better (and have room for a third buffer): bf16, E =
-// 8, 128 rows each, N = 4096, K = 14336 (128 tiles) 191-208 us against 232-270;
-// with 144 tiles (E = 1, 4096 rows, N = 2304, K = 4096) 103 against 78.
+// half the columns then do better (and have room for a third buffer).  us in
+// tiles of 128 and of 256 columns, E = 8, 256 rows each, contraction 4096:
+//   tiles of 256 columns   bf16     grad_input    MXFP4
+//     64                  61,  88    59,  78     26, 37
+//    128                  80,  95    78,  82     33, 38
+//    144                 123,  99   118,  90     50, 39
+//    192                 131, 114   125, 106     54, 43
+// 128 rows each, 4096 outputs, contraction 14336 (128): bf16 191-208 and 232-270,
+// grad_input 178 and 215, MXFP4 71 and 98.
 bool few_tiles(const GroupedArgs& g) {
   const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
   return rows * ((g.nout + 255) / 256) <= 128;
@@ -962,7 +981,11 @@ hipError_t launch_grouped_mm_grad_input(const GroupedArgs& g, hipStream_t s) {
 namespace {
 
 // Tile shapes of grad_weight: narrow outputs take tiles that are narrow, too
-// (and more of them on a compute unit).
+// (and more of them on a compute unit).  us in narrow and in square tiles, E =
+// 64, 512 rows each, bf16, the other side 2048, inputs from HBM:
+//   narrow side      16      64      72      96     128     192     256
+//     few rows   38, 45  45, 49  48, 49  51, 50  52, 54  65, 61  79, 67
+//     few cols   31, 46  37, 49  48, 49  51, 51  53, 53  65, 60  80, 67
 enum class WeightTile { kSquare, kFewRows, kFewCols };
 WeightTile weight_tile(int32_t N, int32_t K) {
   return N <= 64 ? WeightTile::kFewRows : K <= 64 ? WeightTile::kFewCols : WeightTile::kSquare;
