@@ -18,6 +18,7 @@ moeq_status device_status(hipError_t e) { return e == hipSuccess ? MOEQ_OK : MOE
 constexpr int32_t kMaxDim = 1 << 20;     // N and K of a grouped product
 constexpr int64_t kMaxExpertBytes = int64_t(1) << 31;
 constexpr int32_t kMaxRows = 1 << 28;    // M of a grouped product
+constexpr int64_t kMaxBlocks = int64_t(1) << 40;   // of an MXFP4 tensor: sizes in bytes fit 64 bits
 
 // may_be_empty: rows == 0 is allowed, and the data pointers may then be null.
 moeq_status check_mxfp4(const moeq_qweight* q, bool may_be_empty = false) {
@@ -26,6 +27,7 @@ moeq_status check_mxfp4(const moeq_qweight* q, bool may_be_empty = false) {
   if (q->num_experts <= 0 || q->rows < (may_be_empty ? 0 : 1) || q->cols <= 0) return MOEQ_EINVAL;
   if ((q->rows > 0 && (!q->qdata || !q->scale_codes)) || q->scales) return MOEQ_EINVAL;
   if (q->blocksize != MOEQ_MXFP4_BLOCKSIZE || q->cols % MOEQ_MXFP4_BLOCKSIZE != 0) return MOEQ_EBLOCK;
+  if ((int64_t)q->rows * (q->cols / MOEQ_MXFP4_BLOCKSIZE) > kMaxBlocks / q->num_experts) return MOEQ_ESHAPE;
   if (!aligned16(q->qdata) || !aligned16(q->scale_codes)) return MOEQ_EALIGN;
   return MOEQ_OK;
 }

@@ -98,7 +98,8 @@ enum { MOEQ_DTYPE_BF16 = 1, MOEQ_DTYPE_FP32 = 2 };
  * scale_codes must be NULL for plain NF4 and int8.
  * The experts and offload calls below take NF4, NF4_DQ and int8 tensors;
  * MXFP4 tensors belong to the calls that name the format, and any other call
- * returns MOEQ_EFORMAT.
+ * returns MOEQ_EFORMAT.  Those calls return MOEQ_ESHAPE for a tensor of more
+ * than 2^40 blocks.
  */
 typedef struct moeq_qweight {
   int32_t format;

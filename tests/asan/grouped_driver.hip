@@ -97,7 +97,15 @@ static void mxfp4_format() {
   EXPECT(moeq_quantize_mxfp4(w, &bad, nullptr), MOEQ_EALIGN);
   EXPECT(moeq_quantize_mxfp4(at<uint16_t>(kFar + 2), &q, nullptr), MOEQ_EALIGN);
   EXPECT(launches, 0);
-  // the largest tensor that fits the fields: its size fits 64 bits
+  // sizes whose product leaves 64 bits
+  for (int e : {1, 1 << 20, INT_MAX}) {
+    bad = q; bad.num_experts = e; bad.rows = INT_MAX; bad.cols = INT_MAX / 32 * 32;
+    EXPECT(moeq_quantize_mxfp4(w, &bad, nullptr), MOEQ_ESHAPE);
+    EXPECT(moeq_dequantize_mxfp4(&bad, w, nullptr), MOEQ_ESHAPE);
+    EXPECT(moeq_grouped_mm_mxfp4(&q, &bad, at<int32_t>(4), w, nullptr), MOEQ_ESHAPE);
+  }
+  EXPECT(launches, 0);
+  // as many experts as the field takes
   bad = q; bad.num_experts = INT_MAX; bad.rows = 1; bad.cols = 32;
   EXPECT(moeq_quantize_mxfp4(w, &bad, nullptr), MOEQ_OK);
   // neighbours: the buffers touch, and overlap by one 16-byte step
