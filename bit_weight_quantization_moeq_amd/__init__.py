@@ -31,6 +31,8 @@ __all__ = [
     "FMT_MXFP4", "MXFP4_BLOCKSIZE", "moeq_quantize_mxfp4", "moeq_grouped_mm", "moeq_grouped_mm_grad_input",
     "moeq_grouped_mm_grad_weight", "moeq_grouped_mm_grad_weight_workspace_bytes", "moeq_grouped_mm_mxfp4", "moeq_clip_grad_norm_workspace_bytes",
     "moeq_clip_grad_norm",
+    "moeq_grouped_ffn_workspace_bytes", "moeq_grouped_ffn", "moeq_grouped_ffn_backward_workspace_bytes",
+    "moeq_grouped_ffn_backward",
 ]
 
 FMT_NF4 = 1
@@ -107,6 +109,10 @@ def _load():
         "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
         "moeq_grouped_mm_grad_weight_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "moeq_grouped_mm_mxfp4": (I32, [QP, QP, P, P, P]),
+        "moeq_grouped_ffn_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "moeq_grouped_ffn": (I32, [P, P, P, P, I32, I32, I32, I32, P, P, P, SZ, P]),
+        "moeq_grouped_ffn_backward_workspace_bytes": (SZ, [I32, I32, I32, I32]),
+        "moeq_grouped_ffn_backward": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P, P, SZ, P]),
         "moeq_clip_grad_norm_workspace_bytes": (SZ, [I32]),
         "moeq_clip_grad_norm": (I32, [P, I32, ctypes.c_double, P, P, SZ, P]),
     }
@@ -953,6 +959,110 @@ def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
 
 
 _GRAD_DTYPES = {torch.bfloat16: 1, torch.float32: 2}
+
+
+def _workspace_for(workspace, need, dev, stream):
+    """The caller's workspace (its size is checked by the library) or a new one
+    of ``need`` bytes for a call on ``stream``; None where none is needed."""
+    if workspace is not None:
+        return _workspace(workspace, need, dev)
+    return _empty((need,), torch.uint8, dev, stream) if need > 0 else None
+
+
+def _numel(t):
+    return 0 if t is None else t.numel()
+
+
+def _grouped_ffn(x, gate_up, down, offsets, name="x"):
+    """(M, E, H, I) of rows [M, H], gate_up [E, 2I, H], down [E, H, I] (bf16)
+    and offsets [E+1] int32, structurally checked."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    for n, t in (("gate_up", gate_up), ("down", down)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3:
+            raise ValueError(f"{n} must be a 3-D tensor")
+    M, H = x.shape
+    E, _, I = down.shape
+    _dev(x, torch.bfloat16, name)
+    _dev(gate_up, torch.bfloat16, "gate_up", (E, 2 * I, H))
+    _dev(down, torch.bfloat16, "down", (E, H, I))
+    _dev(offsets, torch.int32, "offsets", (E + 1,))
+    return int(M), int(E), int(H), int(I)
+
+
+def moeq_grouped_ffn_workspace_bytes(M, E, H, I):
+    """Workspace bytes :func:`moeq_grouped_ffn` needs (0 if the arguments are invalid)."""
+    return int(_load().moeq_grouped_ffn_workspace_bytes(int(M), int(E), int(H), int(I)))
+
+
+def moeq_grouped_ffn(x, gate_up, down, offsets, save=False, out=None, gu=None, workspace=None, stream=None):
+    """The experts' gated feed-forward block over rows sorted by expert, in
+    bf16: ``out[p] = down[e] @ (silu(g) * u)`` with ``g | u = gate_up[e] @ x[p]``
+    for the rows ``offsets[e] <= p < offsets[e+1]`` of each expert e.  ``x``
+    ``[M, H]``, ``gate_up`` ``[E, 2I, H]`` (gate rows first), ``down``
+    ``[E, H, I]``, ``offsets`` int32 ``[E+1]`` on the device; returns ``out``
+    bf16 ``[M, H]``, with ``save`` (or a buffer ``gu``) also ``gu`` bf16
+    ``[M, 2I]`` for :func:`moeq_grouped_ffn_backward`.  Rows outside
+    ``[offsets[0], offsets[E])`` are not written.  H and I are multiples of 8."""
+    M, E, H, I = _grouped_ffn(x, gate_up, down, offsets)
+    if out is not None:
+        _dev(out, torch.bfloat16, "out", (M, H))
+    if gu is not None:
+        _dev(gu, torch.bfloat16, "gu", (M, 2 * I))
+    dev = _on_device("moeq_grouped_ffn", x, gate_up, down, offsets, out, gu)
+    y = _empty((M, H), torch.bfloat16, dev, stream) if out is None else out
+    if save and gu is None:
+        gu = _empty((M, 2 * I), torch.bfloat16, dev, stream)
+    lib = _load()
+    workspace = _workspace_for(workspace, int(lib.moeq_grouped_ffn_workspace_bytes(M, E, H, I)), dev, stream)
+    with _current(dev):
+        _check(lib.moeq_grouped_ffn(_ptr(x), _ptr(gate_up), _ptr(down), _ptr(offsets), M, E, H, I, _ptr(gu), _ptr(y),
+                                    _ptr(workspace), _numel(workspace), _stream(stream, dev)), "moeq_grouped_ffn")
+    return y if gu is None else (y, gu)
+
+
+def moeq_grouped_ffn_backward_workspace_bytes(M, E, H, I):
+    """Workspace bytes :func:`moeq_grouped_ffn_backward` needs (0 if the arguments are invalid)."""
+    return int(_load().moeq_grouped_ffn_backward_workspace_bytes(int(M), int(E), int(H), int(I)))
+
+
+def moeq_grouped_ffn_backward(grad_out, x, gate_up, down, offsets, gu, dtype=torch.float32, grad_x=None,
+                              grad_gate_up=None, grad_down=None, workspace=None, stream=None):
+    """Gradients of :func:`moeq_grouped_ffn` for ``grad_out`` bf16 ``[M, H]``,
+    from its inputs and the ``gu`` it saved; returns ``(grad_x bf16 [M, H],
+    grad_gate_up [E, 2I, H], grad_down [E, H, I])``, the weights' gradients in
+    ``dtype`` (fp32 or bf16; or that of the buffers given), zeros for an expert
+    without rows.  The sums are fp32 either way, of bf16 ``h``, ``dg`` and
+    ``du``.  Rows of ``grad_x`` outside ``[offsets[0], offsets[E])`` are not
+    written."""
+    M, E, H, I = _grouped_ffn(x, gate_up, down, offsets)
+    _dev(grad_out, torch.bfloat16, "grad_out", (M, H))
+    _dev(gu, torch.bfloat16, "gu", (M, 2 * I))
+    if grad_x is not None:
+        _dev(grad_x, torch.bfloat16, "grad_x", (M, H))
+    given = next((t for t in (grad_gate_up, grad_down) if t is not None), None)
+    if given is not None:
+        dtype = given.dtype if isinstance(given, torch.Tensor) else dtype
+    if dtype not in _GRAD_DTYPES:
+        raise TypeError(f"the weights' gradients must be torch.float32 or torch.bfloat16, got {dtype}")
+    if grad_gate_up is not None:
+        _dev(grad_gate_up, dtype, "grad_gate_up", (E, 2 * I, H))
+    if grad_down is not None:
+        _dev(grad_down, dtype, "grad_down", (E, H, I))
+    dev = _on_device("moeq_grouped_ffn_backward", grad_out, x, gate_up, down, offsets, gu, grad_x, grad_gate_up,
+                     grad_down)
+    dx = _empty((M, H), torch.bfloat16, dev, stream) if grad_x is None else grad_x
+    dgu = _empty((E, 2 * I, H), dtype, dev, stream) if grad_gate_up is None else grad_gate_up
+    dd = _empty((E, H, I), dtype, dev, stream) if grad_down is None else grad_down
+    lib = _load()
+    need = int(lib.moeq_grouped_ffn_backward_workspace_bytes(M, E, H, I))
+    workspace = _workspace_for(workspace, need, dev, stream)
+    with _current(dev):
+        _check(lib.moeq_grouped_ffn_backward(_ptr(grad_out), _ptr(x), _ptr(gate_up), _ptr(down), _ptr(offsets), _ptr(gu),
+                                             M, E, H, I, _GRAD_DTYPES[dtype], _ptr(dx), _ptr(dgu), _ptr(dd),
+                                             _ptr(workspace), _numel(workspace), _stream(stream, dev)),
+               "moeq_grouped_ffn_backward")
+    return dx, dgu, dd
 
 
 def moeq_clip_grad_norm_workspace_bytes(count):

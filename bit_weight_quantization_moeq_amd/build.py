@@ -19,7 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmoeq.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "quant.hip", "route.hip", "experts.hip", "decode.hip", "router.hip",
-           "api_grouped.hip", "mxfp4.hip", "grouped.hip", "clip.hip"]
+           "api_grouped.hip", "mxfp4.hip", "grouped.hip", "clip.hip",
+           "api_ffn.hip", "ffn.hip"]
 ARCH = "gfx950"
 
 # IEEE fp32 division and denormals stay on (no fast-math, no FTZ): the NF4 and

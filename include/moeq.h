@@ -493,6 +493,54 @@ moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, 
                                   uint16_t *out_bf16, void *stream);
 
 /*
+ * The gated feed-forward block of experts over rows sorted by expert, in bf16:
+ * moeq_experts_forward's block for experts that are trained rather than frozen
+ * and packed ("MoE Expert Quantization", Axolotl docs, Expert LoRA targeting).
+ * For rows p with offsets[e] <= p < offsets[e + 1]:
+ *   g | u   = gate_up[e] x[p]          out[p] = down[e] h,  h = silu(g) * u
+ *   x, out    bf16 [M][H]
+ *   gate_up   bf16 [E][2I][H]: rows 0..I-1 the gate, I..2I-1 the up projection
+ *   down      bf16 [E][H][I]
+ *   offsets   int32 [E+1] on the device, as for moeq_grouped_mm
+ *   gu_saved  NULL, or bf16 [M][2I] for g | u, which the backward pass takes
+ *   workspace of moeq_grouped_ffn_workspace_bytes(M, E, H, I), 16-byte aligned
+ * g, u and the sums are fp32; h is rounded to bf16 for the down product, and g
+ * and u are where they are saved.  The same bits from run to run.  Rows of out
+ * and gu_saved outside [offsets[0], offsets[E]) are not written, and such rows
+ * of x never reach a result.  Alignment, overlaps and offsets that do not
+ * ascend as for moeq_grouped_mm.  MOEQ_ESHAPE unless moeq_grouped_mm and
+ * moeq_grouped_mm_grad_input take both products (H and I multiples of 8, 4*I*H
+ * < 2^31).  M == 0 is a valid no-op.
+ */
+size_t moeq_grouped_ffn_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t I);
+moeq_status moeq_grouped_ffn(const uint16_t *x_bf16, const uint16_t *gate_up_bf16, const uint16_t *down_bf16,
+                             const int32_t *offsets, int32_t M, int32_t E, int32_t H, int32_t I, uint16_t *gu_saved,
+                             uint16_t *out_bf16, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients for the incoming grad_out = dL/dout, bf16 [M][H], from the same
+ * x, gate_up, down and offsets and the forward's gu_saved:
+ *   dh = down[e]^T grad_out[p]    s = 1 / (1 + exp(-g))
+ *   dg = dh u s (1 + g (1 - s))   du = dh g s
+ *   grad_x        bf16 [M][H]: gate_up[e]^T (dg | du)
+ *   grad_gate_up  [E][2I][H]: sum over the expert's rows of (dg | du) x[p]^T
+ *   grad_down     [E][H][I]: sum of grad_out[p] h^T, h from the saved g and u
+ *                 both fp32 (dtype MOEQ_DTYPE_FP32) or bf16 (MOEQ_DTYPE_BF16);
+ *                 zeros for an expert without rows
+ *   workspace     of moeq_grouped_ffn_backward_workspace_bytes(M, E, H, I)
+ * dh and every sum are fp32; h, dg and du are rounded to bf16 for the products
+ * that take them, so fp32 weight gradients carry that rounding.  Rows outside
+ * [offsets[0], offsets[E]) as above; M == 0 writes zero weight gradients.
+ * Otherwise as moeq_grouped_ffn.
+ */
+size_t moeq_grouped_ffn_backward_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t I);
+moeq_status moeq_grouped_ffn_backward(const uint16_t *grad_out_bf16, const uint16_t *x_bf16,
+                                      const uint16_t *gate_up_bf16, const uint16_t *down_bf16, const int32_t *offsets,
+                                      const uint16_t *gu_saved, int32_t M, int32_t E, int32_t H, int32_t I,
+                                      int32_t dtype, uint16_t *grad_x_bf16, void *grad_gate_up, void *grad_down,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * The norm of all gradients of a training step, and their clipping:
  *   *norm = sqrt(sum of squares over every tensor)
  *   dst   = src * min(1, max_norm / *norm), in the tensor's own type
