@@ -33,14 +33,18 @@ __all__ = [
     "moeq_clip_grad_norm",
     "moeq_grouped_ffn_workspace_bytes", "moeq_grouped_ffn", "moeq_grouped_ffn_backward_workspace_bytes",
     "moeq_grouped_ffn_backward",
+    "FMT_FP8_ROW", "FMT_FP8_TILE", "FP8_BLOCKSIZE", "moeq_quantize_fp8", "moeq_grouped_mm_fp8",
 ]
 
 FMT_NF4 = 1
 FMT_INT8_ROWWISE = 2
 FMT_NF4_DQ = 3
 FMT_MXFP4 = 4
+FMT_FP8_ROW = 5
+FMT_FP8_TILE = 6
 NF4_BLOCKSIZE = 64
 MXFP4_BLOCKSIZE = 32
+FP8_BLOCKSIZE = 128
 DQ_GROUP = 256
 ABI_VERSION = 3
 NOALLOC_SCRATCH_BYTES = 64 << 20
@@ -109,6 +113,9 @@ def _load():
         "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
         "moeq_grouped_mm_grad_weight_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "moeq_grouped_mm_mxfp4": (I32, [QP, QP, P, P, P]),
+        "moeq_quantize_fp8": (I32, [P, QP, P]),
+        "moeq_dequantize_fp8": (I32, [QP, P, P]),
+        "moeq_grouped_mm_fp8": (I32, [QP, QP, P, P, P]),
         "moeq_grouped_ffn_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "moeq_grouped_ffn": (I32, [P, P, P, P, I32, I32, I32, I32, P, P, P, SZ, P]),
         "moeq_grouped_ffn_backward_workspace_bytes": (SZ, [I32, I32, I32, I32]),
@@ -255,6 +262,15 @@ def _workspace(workspace, need, device):
     return workspace
 
 
+_FP8_FORMATS = (FMT_FP8_ROW, FMT_FP8_TILE)
+
+
+def _fp8_blocks(fmt, rows, cols):
+    """Shape of an expert's scales."""
+    across = (cols + FP8_BLOCKSIZE - 1) // FP8_BLOCKSIZE
+    return (rows if fmt == FMT_FP8_ROW else (rows + FP8_BLOCKSIZE - 1) // FP8_BLOCKSIZE, across)
+
+
 class QWeight:
     """A quantized expert tensor ``[E, rows, cols]``: packed codes plus scales.
 
@@ -264,15 +280,18 @@ class QWeight:
     ``qdata``, ``scale_codes`` uint8 ``[E, rows*cols/64]`` and ``scales``
     fp32 group scales ``[E, ceil(rows*cols/64 / 256)]``.  MXFP4: ``qdata``
     uint8 ``[E, rows, cols/2]`` (the even column in the low nibble),
-    ``scale_codes`` uint8 ``[E, rows, cols/32]`` and no ``scales``.  Plain
-    tensors, so they serialise with ``torch.save``.
+    ``scale_codes`` uint8 ``[E, rows, cols/32]`` and no ``scales``.  FP8:
+    ``qdata`` float8_e4m3fn ``[E, rows, cols]``, ``scales`` fp32 ``[E, rows,
+    ceil(cols/128)]`` (FMT_FP8_ROW) or ``[E, ceil(rows/128), ceil(cols/128)]``
+    (FMT_FP8_TILE).  Plain tensors, so they serialise with ``torch.save``.
     """
 
     def __init__(self, fmt, num_experts, rows, cols, qdata, scales, scale_codes=None):
         self.format = fmt
         self.num_experts, self.rows, self.cols = int(num_experts), int(rows), int(cols)
         self.blocksize = {FMT_NF4: NF4_BLOCKSIZE, FMT_NF4_DQ: NF4_BLOCKSIZE,
-                          FMT_MXFP4: MXFP4_BLOCKSIZE}.get(fmt, self.cols)
+                          FMT_MXFP4: MXFP4_BLOCKSIZE, FMT_FP8_ROW: FP8_BLOCKSIZE,
+                          FMT_FP8_TILE: FP8_BLOCKSIZE}.get(fmt, self.cols)
         self.qdata, self.scales, self.scale_codes = qdata, scales, scale_codes
 
     @classmethod
@@ -294,6 +313,9 @@ class QWeight:
             q = torch.empty((E, R, C // 2), dtype=torch.uint8, device=device)
             s = None
             codes = torch.empty((E, R, C // MXFP4_BLOCKSIZE), dtype=torch.uint8, device=device)
+        elif fmt in _FP8_FORMATS:
+            q = torch.empty((E, R, C), dtype=torch.float8_e4m3fn, device=device)
+            s = torch.empty((E, *_fp8_blocks(fmt, R, C)), dtype=torch.float32, device=device)
         else:
             raise ValueError(f"unknown format {fmt}")
         return cls(fmt, E, R, C, q, s, codes)
@@ -335,6 +357,9 @@ class QWeight:
             return [("qdata", (E, R, C), torch.int8), ("scales", (E, R), torch.float32)]
         if self.format == FMT_MXFP4:
             return [("qdata", (E, R, C // 2), torch.uint8), ("scale_codes", (E, R, C // MXFP4_BLOCKSIZE), torch.uint8)]
+        if self.format in _FP8_FORMATS:
+            return [("qdata", (E, R, C), torch.float8_e4m3fn),
+                    ("scales", (E, *_fp8_blocks(self.format, R, C)), torch.float32)]
         raise ValueError(f"unknown format {self.format}")
 
     def validate_layout(self):
@@ -344,6 +369,8 @@ class QWeight:
             raise ValueError(f"NF4 needs cols % {NF4_BLOCKSIZE} == 0, got cols={self.cols}")
         if self.format == FMT_MXFP4 and self.cols % MXFP4_BLOCKSIZE != 0:
             raise ValueError(f"MXFP4 needs cols % {MXFP4_BLOCKSIZE} == 0, got cols={self.cols}")
+        if self.format in _FP8_FORMATS and self.cols % 16 != 0:
+            raise ValueError(f"FP8 needs cols % 16 == 0, got cols={self.cols}")
         lay = self.layout()
         if self.format not in (FMT_NF4_DQ, FMT_MXFP4) and self.scale_codes is not None:
             raise ValueError("scale_codes is only used by the double-quantized NF4 and the MXFP4 format")
@@ -495,6 +522,36 @@ def moeq_quantize_mxfp4(w, out=None, stream=None):
     return q
 
 
+def moeq_quantize_fp8(w, fmt=FMT_FP8_TILE, out=None, stream=None):
+    """bf16 ``[E, rows, cols]`` (weights) or ``[rows, cols]`` (activations;
+    E = 1) -> FP8 :class:`QWeight`: E4M3 codes with an fp32 scale for each 128
+    columns of a row (``FMT_FP8_ROW``) or each 128 x 128 tile
+    (``FMT_FP8_TILE``); ``out``, where given, says which.  A block with an
+    infinity or a NaN becomes NaN.  cols is a multiple of 16."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a [E, rows, cols] or [rows, cols] tensor")
+    _dev(w, torch.bfloat16, "w")
+    shape = tuple(w.shape) if w.dim() == 3 else (1, *w.shape)
+    if shape[2] % 16 != 0:
+        raise ValueError(f"FP8 needs cols % 16 == 0, got cols={shape[2]}")
+    if out is not None:
+        _match_qweight(out, shape, _FP8_FORMATS, "out")
+        out.validate_layout()
+    elif fmt not in _FP8_FORMATS:
+        raise ValueError(f"fmt must be one of {_FP8_FORMATS}, got {fmt}")
+    dev = _on_device("moeq_quantize_fp8", w, *(out._tensors() if out is not None else []))
+    q = out
+    if out is None:
+        E, R, C = shape
+        q = QWeight(fmt, E, R, C, _empty((E, R, C), torch.float8_e4m3fn, dev, stream),
+                    _empty((E, *_fp8_blocks(fmt, R, C)), torch.float32, dev, stream))
+    if w.numel():
+        qc = q._desc()
+        with _current(dev):
+            _check(_load().moeq_quantize_fp8(_ptr(w), ctypes.byref(qc), _stream(stream, dev)), "moeq_quantize_fp8")
+    return q
+
+
 def moeq_dequantize(q, out=None, stream=None):
     """:class:`QWeight` -> bf16 ``[E, rows, cols]``."""
     if not isinstance(q, QWeight):
@@ -503,15 +560,15 @@ def moeq_dequantize(q, out=None, stream=None):
     if out is not None:
         _dev(out, torch.bfloat16, "out", q.shape)
     dev = _on_device("moeq_dequantize", *q._tensors(), out)
-    if q.format == FMT_MXFP4:
+    if q.format == FMT_MXFP4 or q.format in _FP8_FORMATS:
+        name = "moeq_dequantize_mxfp4" if q.format == FMT_MXFP4 else "moeq_dequantize_fp8"
         if out is None:
             out = _empty(q.shape, torch.bfloat16, dev, stream)
         qc = q._desc()
         if out.numel() == 0:
             return out
         with _current(dev):
-            _check(_load().moeq_dequantize_mxfp4(ctypes.byref(qc), _ptr(out), _stream(stream, dev)),
-                   "moeq_dequantize_mxfp4")
+            _check(getattr(_load(), name)(ctypes.byref(qc), _ptr(out), _stream(stream, dev)), name)
         return out
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.qdata.device)
@@ -929,16 +986,14 @@ def moeq_grouped_mm_grad_weight(grad_out, x, offsets, dtype=torch.float32, grad_
     return dw
 
 
-def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
-    """:func:`moeq_grouped_mm` with both operands MXFP4 :class:`QWeight`:
-    ``x`` ``[1, M, K]`` (:func:`moeq_quantize_mxfp4` of the sorted rows), ``w``
-    ``[E, N, K]``; bf16 ``[M, N]``.  The scaled products run on the 4-bit
-    matrix instructions with fp32 sums.  N is a multiple of 8."""
-    for name, q in (("x", x), ("w", w)):
+def _grouped_quantized(where, x, w, offsets, formats, out, stream):
+    """A product of two :class:`QWeight` grouped by expert, by the entry point
+    ``where``; formats: (name, tag) of x and of w."""
+    for name, q, (kind, fmt) in (("x", x, formats[0]), ("w", w, formats[1])):
         if not isinstance(q, QWeight):
             raise TypeError(f"{name} must be a QWeight")
-        if q.format != FMT_MXFP4:
-            raise ValueError(f"{name} has format {q.format}, expected MXFP4 ({FMT_MXFP4})")
+        if q.format != fmt:
+            raise ValueError(f"{name} has format {q.format}, expected {kind} ({fmt})")
         q.validate_layout()
     if x.num_experts != 1:
         raise ValueError(f"x must describe [1, M, K], got {x.shape}")
@@ -948,14 +1003,32 @@ def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
     M, N = x.rows, w.rows
     if out is not None:
         _dev(out, torch.bfloat16, "out", (M, N))
-    dev = _on_device("moeq_grouped_mm_mxfp4", *x._tensors(), *w._tensors(), offsets, out)
+    dev = _on_device(where, *x._tensors(), *w._tensors(), offsets, out)
     y = _empty((M, N), torch.bfloat16, dev, stream) if out is None else out
     if M:
         xc, wc = x._desc(), w._desc()
         with _current(dev):
-            _check(_load().moeq_grouped_mm_mxfp4(ctypes.byref(xc), ctypes.byref(wc), _ptr(offsets), _ptr(y),
-                                                 _stream(stream, dev)), "moeq_grouped_mm_mxfp4")
+            _check(getattr(_load(), where)(ctypes.byref(xc), ctypes.byref(wc), _ptr(offsets), _ptr(y),
+                                           _stream(stream, dev)), where)
     return y
+
+
+def moeq_grouped_mm_mxfp4(x, w, offsets, out=None, stream=None):
+    """:func:`moeq_grouped_mm` with both operands MXFP4 :class:`QWeight`:
+    ``x`` ``[1, M, K]`` (:func:`moeq_quantize_mxfp4` of the sorted rows), ``w``
+    ``[E, N, K]``; bf16 ``[M, N]``.  The scaled products run on the 4-bit
+    matrix instructions with fp32 sums.  N is a multiple of 8."""
+    return _grouped_quantized("moeq_grouped_mm_mxfp4", x, w, offsets, (("MXFP4", FMT_MXFP4),) * 2, out, stream)
+
+
+def moeq_grouped_mm_fp8(x, w, offsets, out=None, stream=None):
+    """:func:`moeq_grouped_mm` with both operands FP8 :class:`QWeight`: ``x``
+    ``[1, M, K]`` with row scales (:func:`moeq_quantize_fp8` of the sorted rows,
+    ``FMT_FP8_ROW``), ``w`` ``[E, N, K]`` with tile scales (``FMT_FP8_TILE``);
+    bf16 ``[M, N]``.  The codes' products run on the 8-bit matrix instructions,
+    summed and scaled in fp32 block by block.  N is a multiple of 8."""
+    formats = (("FP8 with row scales", FMT_FP8_ROW), ("FP8 with tile scales", FMT_FP8_TILE))
+    return _grouped_quantized("moeq_grouped_mm_fp8", x, w, offsets, formats, out, stream)
 
 
 _GRAD_DTYPES = {torch.bfloat16: 1, torch.float32: 2}

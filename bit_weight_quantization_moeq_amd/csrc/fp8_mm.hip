@@ -1,0 +1,356 @@
+// Products grouped by expert with both operands in FP8 (gfx950), rows of x
+// with a scale for each 128 columns, weights with one for each 128 x 128 tile:
+//
+//   y[p][n] = sum over blocks b of sx[p][b] sw[n / 128][b] (sum over k in b of x[p][k] w[e][n][k])
+//
+// The matrix instructions' own block scales are powers of two, so fp32 scales
+// are applied to their results.  v_mfma_f32_16x16x128_f8f6f4 takes a whole
+// block of the contraction: its result, from a zero accumulator, is the inner
+// sum, and four FMAs a lane add it to the fp32 sums, in the time of the next
+// matrix instructions.  The weights' columns are the A operand, so that a lane
+// holds four columns of one row: the scale of a result is one value a lane, and
+// the weights' a scalar of the wave.
+//
+// Inside the instruction, eight consecutive products are cut off at 2^-13 of the
+// largest one's power of two before they are added; the sums of eights, and all
+// that follows, are fp32.  For random operands that is 2^-12 of the result (rms;
+// the output's rounding to bf16 2^-9.2).  The way around it, bf16 operands for
+// the 16-bit instructions, takes twice the time.
+//
+// Tiles, LDS layout and copies are those of grouped_tile.h; a step of 128 bytes
+// is one block.
+#include "grouped_tile.h"
+
+#include "fp8.h"
+
+namespace moeq {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+struct Fp8Args : GroupedArgs {
+  const float* xs;   // [M][nkb]
+  const float* ws;   // [E][nrb][nkb]
+  int32_t nkb;       // blocks of the contraction
+};
+
+__device__ __forceinline__ f32x4 mfma_fp8(const u32x4 (&a)[2], const u32x4 (&b)[2]) {
+  const i32x8 x = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w, (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
+  const i32x8 y = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w, (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
+  // operand formats 0: E4M3; scales of 1
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, (f32x4){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7f7f7f7f, 0,
+                                                          0x7f7f7f7f);
+}
+
+// kNWN x kNWM waves, each kTN blocks of 16 columns by kTM blocks of 16 rows.
+template <int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+struct Fp8Tile {
+  static constexpr int kNW = kNWN * kNWM, kCols = 16 * kTN * kNWN, kRows = 16 * kTM * kNWM;
+  using A = Side<false, kCols, kNW>;
+  using B = Side<false, kRows, kNW>;
+  static_assert(kFp8Block % (16 * kTN) == 0, "a wave's columns have one scale");
+  static_assert(kRows <= 64 * kNW, "a lane per row's scales");
+  static constexpr int kBytesB = kBufs * A::kBytes, kScales = kBytesB + kBufs * B::kBytes;
+  static constexpr int kScaleBuf = 16 * 64 * ((kRows + 63) / 64);   // a row's scales of four steps
+  static constexpr int kOutPitch = 32 * kTN + 16, kPiece = 2 * 16 * kOutPitch;
+  static constexpr int kLds = imax(kScales + 2 * kScaleBuf, kNW * kPiece);
+  static constexpr int kInstr = A::kInstr + B::kInstr;
+
+  __device__ __forceinline__ static void frag(const char* tile, int c0, int lane, u32x4 (&f)[2]) {
+    const char* p = tile + (c0 + (lane & 15)) * kStepBytes;
+    const int swz = A::swz(lane & 15), grp = lane >> 4;
+    f[0] = *reinterpret_cast<const u32x4*>(p + 16 * (grp ^ swz));
+    f[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((4 + grp) ^ swz));
+  }
+
+  __device__ __forceinline__ static void run(char* smem, const Fp8Args& g, int e, int row0, int nrows, int c0) {
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wn = wave % kNWN, wm = wave / kNWN, l16 = lane & 15, grp = lane >> 4;
+    const int ncols = min(kCols, g.nout - c0), nkb = g.nkb;
+    A a;
+    B b;
+    a.init(static_cast<const char*>(g.w) + ((int64_t)e * g.nout + c0) * g.kc, (int64_t)ncols * g.kc, g.kc, g.kc, wave, lane);
+    b.init(static_cast<const char*>(g.x) + (int64_t)row0 * g.kc, (int64_t)nrows * g.kc, g.kc, g.kc, wave, lane);
+    uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
+    asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
+    const char* xs = reinterpret_cast<const char*>(g.xs + (int64_t)row0 * nkb);
+    const int64_t xs_bytes = (int64_t)nrows * nkb * 4;
+    // the weights' scales, 64 steps at a time, one a lane
+    const int tile = min((c0 + 16 * kTN * wn) / kFp8Block, fp8_blocks(g.nout) - 1);
+    const float* ws = g.ws + ((int64_t)e * fp8_blocks(g.nout) + tile) * nkb;
+    float wsv = ws[min(lane, nkb - 1)];
+
+    auto dma_a = [&](int ks, int i) {
+      a.template dma<false>(ks, i, wave, lds0 + (uint32_t)(ks % kBufs * A::kBytes));
+    };
+    auto dma_b = [&](int ks, int i) {
+      b.template dma<false>(ks, i, wave, lds0 + (uint32_t)(kBytesB + ks % kBufs * B::kBytes));
+    };
+    // scales of steps 4 q .. + 3 (what lies behind a row's last one is not used)
+    auto dma_scales = [&](int q) {
+      if (64 * wave < kRows) {
+        const uint32_t off = ((uint32_t)(64 * wave + lane) * (uint32_t)nkb + 4u * (uint32_t)q) * 4u;
+        dma16<false>(xs, xs_bytes, off, lds0 + (uint32_t)(kScales + (q & 1) * kScaleBuf + 1024 * wave));
+      }
+    };
+    auto row_scale = [&](int ks, int m) {
+      return *reinterpret_cast<const float*>(smem + kScales + ((ks >> 2) & 1) * kScaleBuf +
+                                             16 * (16 * (kTM * wm + m) + l16) + 4 * (ks & 3));
+    };
+    auto frag_a = [&](int ks, int n, u32x4 (&f)[2]) { frag(smem + ks % kBufs * A::kBytes, 16 * (kTN * wn + n), lane, f); };
+    auto frag_b = [&](int ks, int m, u32x4 (&f)[2]) {
+      frag(smem + kBytesB + ks % kBufs * B::kBytes, 16 * (kTM * wm + m), lane, f);
+    };
+
+    dma_scales(0);
+    for (int p = 0; p < kBufs; ++p) {
+      for (int i = 0; i < A::kInstr; ++i) dma_a(p, i);
+      for (int i = 0; i < B::kInstr; ++i) dma_b(p, i);
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 1) * kInstr>);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+
+    // the results of the last kLate matrix instructions are on their way
+    constexpr int kLate = 2, kRing = 4, kSlots = kTN * kTM;
+    static_assert(kSlots % kRing == 0 && kTN >= kLate, "a step is whole turns of the ring, and a result one block of rows late");
+    f32x4 acc[kTN][kTM], part[kRing];
+    u32x4 fa[kTN][2], fb[2][2];
+    float sx[2], before = 0.f, now = 0.f;   // scales of the last two blocks of rows
+#pragma unroll
+    for (int n = 0; n < kTN; ++n) {
+#pragma unroll
+      for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      frag_a(0, n, fa[n]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) part[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    frag_b(0, 0, fb[0]);
+    sx[0] = row_scale(0, 0);
+    static_assert(kTM % 2 == 0, "operands in two turns");
+    // Step ks: a result is added kLate matrix instructions later.  The barrier stands before the last block of rows:
+    // by then every wave has the step's operands in registers, so that the
+    // next step's are read, and its buffers filled anew, from there on.
+    for (int ks = 0; ks < nkb; ++ks) {
+      if (ks != 0 && (ks & 63) == 0) wsv = ws[min(ks + lane, nkb - 1)];
+      const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), ks & 63));
+#pragma unroll
+      for (int m = 0; m < kTM; ++m) {
+        const bool last = m + 1 == kTM;
+        if (last) {
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 2) * kInstr>);
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+          if ((ks & 3) == 0) dma_scales((ks >> 2) + 1);
+        }
+        before = now;
+        now = sx[m & 1] * sw;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int n = 0; n < kTN; ++n) {
+          const int slot = m * kTN + n, due = (slot + kSlots - kLate) % kSlots;
+          part[slot % kRing] = mfma_fp8(fa[n], fb[m & 1]);
+          const f32x4 r = part[due % kRing];
+          f32x4& s = acc[due % kTN][due / kTN];
+          const float scale = due / kTN == m ? now : before;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(r[i], scale, s[i]);
+          if (n == 0) {
+            frag_b(last ? ks + 1 : ks, (m + 1) % kTM, fb[(m + 1) & 1]);
+            sx[(m + 1) & 1] = row_scale(last ? ks + 1 : ks, (m + 1) % kTM);
+          }
+          if (last) {
+            frag_a(ks + 1, n, fa[n]);
+#pragma unroll
+            for (int i = 0; i < A::kInstr; ++i)
+              if (i * kTN / A::kInstr == n) dma_a(ks + kBufs, i);
+#pragma unroll
+            for (int i = 0; i < B::kInstr; ++i)
+              if (i * kTN / B::kInstr == n) dma_b(ks + kBufs, i);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+#pragma unroll
+    for (int slot = kSlots - kLate; slot < kSlots; ++slot) {
+      f32x4& r = part[slot % kRing];
+      mfma_done(r);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[slot % kTN][kTM - 1][i] = __builtin_fmaf(r[i], now, acc[slot % kTN][kTM - 1][i]);
+    }
+    __builtin_amdgcn_s_waitcnt(0);   // copies of steps past the end
+    __syncthreads();
+
+    // out, 16 rows at a time through the wave's own piece of LDS (two in turn)
+    char* piece = smem + wave * kPiece;
+    constexpr int kLanes = 2 * kTN;   // per row, 8 columns each
+    const int c = 16 * kTN * wn + 8 * (lane % kLanes);
+    uint16_t* out = static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.nout + c0 + c;
+#pragma unroll
+    for (int m = 0; m < kTM; ++m) {
+      const int r0 = 16 * (kTM * wm + m);
+      if (r0 >= nrows) break;
+      char* buf = piece + (m & 1) * 16 * kOutPitch;
+#pragma unroll
+      for (int n = 0; n < kTN; ++n)
+        *reinterpret_cast<uint2*>(buf + l16 * kOutPitch + 2 * (16 * n + 4 * grp)) =
+            make_uint2(pack_bf16x2(acc[n][m][0], acc[n][m][1]), pack_bf16x2(acc[n][m][2], acc[n][m][3]));
+      // (a wave's LDS accesses are done in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < (kLanes + 3) / 4; ++u) {
+        const int r = u * (64 / kLanes) + lane / kLanes;
+        if (r < 16 && r0 + r < nrows && c < ncols)
+          __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(buf + r * kOutPitch + 16 * (lane % kLanes)),
+                                      reinterpret_cast<u32x4*>(out + (int64_t)(r0 + r) * g.nout));
+      }
+    }
+  }
+};
+
+template <int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void fp8_rows_kernel(Fp8Args g) {
+  using Big = Fp8Tile<kNWN, kNWM, kTN, kTM, kBufs>;
+  __shared__ __attribute__((aligned(16))) char smem[Big::kLds];
+  int e, row0, nrows, ct;
+  if (!find_tile(g, Big::kRows, (g.nout + Big::kCols - 1) / Big::kCols, e, row0, nrows, ct)) return;
+  const int c0 = ct * Big::kCols;
+  // blocks of 16 rows per wave: as few as the tile's rows need, by twos
+  if constexpr (kTM > 6)
+    if (nrows > 6 * 16 * kNWM) return Fp8Tile<kNWN, kNWM, kTN, 8, kBufs>::run(smem, g, e, row0, nrows, c0);
+  if constexpr (kTM > 4)
+    if (nrows > 4 * 16 * kNWM) return Fp8Tile<kNWN, kNWM, kTN, 6, kBufs>::run(smem, g, e, row0, nrows, c0);
+  if constexpr (kTM > 2)
+    if (nrows > 2 * 16 * kNWM) return Fp8Tile<kNWN, kNWM, kTN, 4, kBufs>::run(smem, g, e, row0, nrows, c0);
+  Fp8Tile<kNWN, kNWM, kTN, 2, kBufs>::run(smem, g, e, row0, nrows, c0);
+}
+
+// Few rows per expert: the weights stream past at most 16 rows, 16 columns a
+// work item, straight into the matrix instructions' operands, as in the other
+// formats' form.  A unit is two blocks of the contraction (256 bytes of a row).
+constexpr int kFewWaves = 4;
+
+template <bool kSplit>
+__global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g) {
+  constexpr int kCols = kSplit ? 16 : 16 * kFewWaves;   // of a workgroup
+  __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][64];
+  int e, row0, nrows, ct;
+  if (!find_tile(g, 16, (g.nout + kCols - 1) / kCols, e, row0, nrows, ct)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, grp = lane >> 4, nkb = g.nkb;
+  const int c0 = ct * kCols + (kSplit ? 0 : 16 * wave), ncols = min(16, g.nout - c0);
+  if (!kSplit && ncols <= 0) return;   // (no barrier there)
+  const __amdgpu_buffer_rsrc_t rx = buffer(static_cast<const char*>(g.x) + (int64_t)row0 * g.kc, (int64_t)nrows * g.kc);
+  const __amdgpu_buffer_rsrc_t rw =
+      buffer(static_cast<const char*>(g.w) + ((int64_t)e * g.nout + c0) * g.kc, (int64_t)ncols * g.kc);
+  const float* xs = g.xs + (int64_t)(row0 + min(l16, nrows - 1)) * nkb;   // (rows that are not there are not stored)
+  const float* ws = g.ws + ((int64_t)e * fp8_blocks(g.nout) + c0 / kFp8Block) * nkb;
+
+  struct Unit {
+    u32x4 w[2][2], x[2][2];
+    float s[2], t[2];
+  };
+  auto load = [&](Unit& v, int u) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int at = u * 256 + 128 * j + 64 * k + 16 * grp;
+        const uint32_t off = at < g.kc ? (uint32_t)l16 * (uint32_t)g.kc + (uint32_t)at : kPast;
+        v.w[j][k] = buffer_load16(rw, off);
+        v.x[j][k] = buffer_load16(rx, off);
+      }
+      const int b = min(2 * u + j, nkb - 1);   // (past the end the codes are zeros)
+      v.s[j] = xs[b];
+      v.t[j] = ws[b];
+    }
+  };
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Unit& v, int u) {
+    f32x4 r[2] = {mfma_fp8(v.w[0], v.x[0]), mfma_fp8(v.w[1], v.x[1])};
+    mfma_done(r[0]);
+    mfma_done(r[1]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (2 * u + j < nkb) {
+        const float s = v.s[j] * v.t[j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(r[j][i], s, acc[i]);
+      }
+  };
+  const int units = (nkb + 1) / 2;
+  constexpr int kStep = kSplit ? kFewWaves : 1;
+  Unit va, vb;
+  int u = kSplit ? wave : 0;
+  if (u < units) load(va, u);
+  while (u < units) {
+    if (u + kStep < units) load(vb, u + kStep);
+    use(va, u);
+    u += kStep;
+    if (u >= units) break;
+    if (u + kStep < units) load(va, u + kStep);
+    use(vb, u);
+    u += kStep;
+  }
+  if constexpr (kSplit) {
+    part[wave][lane] = acc;
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) {
+      const f32x4 q = part[v][lane];
+      acc.x += q.x; acc.y += q.y; acc.z += q.z; acc.w += q.w;
+    }
+  }
+  // the lane holds columns 4 (lane / 16) .. + 3 of row lane % 16
+  if (l16 < nrows && 4 * grp < ncols)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + l16) * g.nout + c0 + 4 * grp) =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+template <int kNWN, int kNWM, int kTN, int kTM, int kBufs>
+hipError_t launch_rows(const Fp8Args& g, hipStream_t s) {
+  using Big = Fp8Tile<kNWN, kNWM, kTN, kTM, kBufs>;
+  const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
+  const int64_t grid = items_grid(((int64_t)g.M / Big::kRows + std::min(g.E, g.M)) * ncol);
+  fp8_rows_kernel<kNWN, kNWM, kTN, kTM, kBufs><<<(unsigned)grid, 64 * kNWN * kNWM, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+hipError_t launch_few_rows(const Fp8Args& g, hipStream_t s) {
+  const int64_t tiles = (g.nout + 15) / 16, slots = (int64_t)g.M / 16 + std::min(g.E, g.M);
+  if (g.nkb >= 4 * kFewWaves || slots * tiles < 4096)
+    fp8_few_rows_kernel<true><<<(unsigned)items_grid(slots * tiles), 64 * kFewWaves, 0, s>>>(g);
+  else
+    fp8_few_rows_kernel<false>
+        <<<(unsigned)items_grid(slots * ((tiles + kFewWaves - 1) / kFewWaves)), 64 * kFewWaves, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+bool streams(const GroupedArgs& g) {
+  const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
+  // A grid holds less than 2^32 threads; beyond that the tiles serve.
+  return (g.M <= 4 * g.E || g.nout <= 16) && items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
+}
+
+bool few_tiles(const GroupedArgs& g) {
+  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
+  return rows * ((g.nout + 255) / 256) <= 128;
+}
+
+}  // namespace
+
+hipError_t launch_grouped_mm_fp8(const GroupedArgs& args, const float* x_scales, const float* w_scales, hipStream_t s) {
+  Fp8Args g;
+  static_cast<GroupedArgs&>(g) = args;
+  g.xs = x_scales;
+  g.ws = w_scales;
+  g.nkb = fp8_blocks(args.kc);
+  if (streams(g)) return launch_few_rows(g, s);
+  if (few_tiles(g)) return launch_rows<4, 2, 2, 8, 3>(g, s);
+  return launch_rows<4, 2, 4, 8, 2>(g, s);
+}
+
+}  // namespace moeq

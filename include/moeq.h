@@ -35,6 +35,7 @@ extern "C" {
 #define MOEQ_NF4_BLOCKSIZE 64
 #define MOEQ_DQ_GROUP 256 /* NF4 blocks per double-quantization group */
 #define MOEQ_MXFP4_BLOCKSIZE 32
+#define MOEQ_FP8_BLOCKSIZE 128
 #define MOEQ_MAX_EXPERTS 1024
 
 typedef int32_t moeq_status;
@@ -50,7 +51,14 @@ enum {
   MOEQ_EDEVICE = -7     /* a HIP call failed                                         */
 };
 
-enum { MOEQ_FMT_NF4 = 1, MOEQ_FMT_INT8_ROWWISE = 2, MOEQ_FMT_NF4_DQ = 3, MOEQ_FMT_MXFP4 = 4 };
+enum {
+  MOEQ_FMT_NF4 = 1,
+  MOEQ_FMT_INT8_ROWWISE = 2,
+  MOEQ_FMT_NF4_DQ = 3,
+  MOEQ_FMT_MXFP4 = 4,
+  MOEQ_FMT_FP8_ROW = 5,
+  MOEQ_FMT_FP8_TILE = 6
+};
 
 /* Element types of gradients. */
 enum { MOEQ_DTYPE_BF16 = 1, MOEQ_DTYPE_FP32 = 2 };
@@ -93,13 +101,22 @@ enum { MOEQ_DTYPE_BF16 = 1, MOEQ_DTYPE_FP32 = 2 };
  *   scale_codes  uint8 [E][rows*cols/32]: one byte s per block of 32 columns,
  *                the scale 2^(s - 127); s = 255 makes the whole block NaN.
  *   scales       NULL.
+ * FP8 (blocksize 128, cols % 16 == 0): E4M3 codes (OCP 8-bit floating point,
+ * three fraction bits, 448 the largest, no infinities) with an fp32 scale for
+ * each 128 columns of a row (format MOEQ_FMT_FP8_ROW, for activations) or each
+ * 128 x 128 tile of an expert (MOEQ_FMT_FP8_TILE, for weights); last blocks and
+ * tiles may be smaller:
+ *   qdata        uint8 [E][rows][cols]: codes.
+ *   scales       fp32 [E][rows][ceil(cols/128)], or
+ *                fp32 [E][ceil(rows/128)][ceil(cols/128)].
+ *   scale_codes  NULL.
  * Since blocks and groups never straddle an expert, &qdata[e] / &scales[e]
  * (and &scale_codes[e]) with num_experts = 1 describe expert e alone.
  * scale_codes must be NULL for plain NF4 and int8.
  * The experts and offload calls below take NF4, NF4_DQ and int8 tensors;
- * MXFP4 tensors belong to the calls that name the format, and any other call
- * returns MOEQ_EFORMAT.  Those calls return MOEQ_ESHAPE for a tensor of more
- * than 2^40 blocks.
+ * MXFP4 and FP8 tensors belong to the calls that name the format, and any other
+ * call returns MOEQ_EFORMAT.  Those calls return MOEQ_ESHAPE for a tensor of
+ * more than 2^40 blocks.
  */
 typedef struct moeq_qweight {
   int32_t format;
@@ -491,6 +508,35 @@ size_t moeq_grouped_mm_grad_weight_workspace_bytes(int32_t M, int32_t E, int32_t
  */
 moeq_status moeq_grouped_mm_mxfp4(const moeq_qweight *x, const moeq_qweight *w, const int32_t *offsets,
                                   uint16_t *out_bf16, void *stream);
+
+/*
+ * Quantize to FP8: w_bf16 bf16 [E][rows][cols] (16-byte aligned; weights, or
+ * activations with E = 1); dst of format MOEQ_FMT_FP8_ROW or MOEQ_FMT_FP8_TILE
+ * says what shares a scale, 16-byte aligned qdata.  For each block, amax its
+ * largest magnitude: scale = fp32(amax / 448), code = the E4M3 value nearest to
+ * 448 w / amax, ties to the even code; a block of zeros stores scale 0 and zero
+ * codes (of either sign).  A block with an infinity or a NaN stores a NaN scale and
+ * zero codes.  (Below amax = 2^-117 the scale is subnormal and loses bits.)
+ * MOEQ_EINVAL for buffers that overlap, here and in moeq_dequantize_fp8.
+ */
+moeq_status moeq_quantize_fp8(const uint16_t *w_bf16, const moeq_qweight *dst, void *stream);
+
+/* FP8 -> bf16 [E][rows][cols], 16-byte aligned: bf16_rne(fp32(code * scale)). */
+moeq_status moeq_dequantize_fp8(const moeq_qweight *src, uint16_t *out_bf16, void *stream);
+
+/*
+ * moeq_grouped_mm with both operands in FP8: x one "expert" of M rows
+ * ([1][M][K], MOEQ_FMT_FP8_ROW), w [E][N][K] of MOEQ_FMT_FP8_TILE.  The codes'
+ * products are summed over each block of 128 columns, multiplied by fp32(x's
+ * scale * w's scale) and added in fp32; the result is rounded once to bf16.
+ * The sums are fp32 ones, but for the 8-bit matrix instructions' alignment:
+ * eight consecutive products are cut off at 2^-13 of the largest one's power of
+ * two.  A block with a NaN scale makes the outputs that it enters NaN.
+ * Otherwise as moeq_grouped_mm; x with rows == 0 (its data pointers may then be
+ * NULL) is a valid no-op.
+ */
+moeq_status moeq_grouped_mm_fp8(const moeq_qweight *x, const moeq_qweight *w, const int32_t *offsets,
+                                uint16_t *out_bf16, void *stream);
 
 /*
  * The gated feed-forward block of experts over rows sorted by expert, in bf16:

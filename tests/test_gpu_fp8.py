@@ -1,0 +1,307 @@
+"""GPU: FP8 with a scale for each block of 128 (codes and scales bit for bit
+against the 64-bit oracle) and the grouped product over it.
+
+Tolerance of a product, per output.  The 8-bit matrix instructions add eight
+consecutive products after cutting each off at 2^-13 of 2^E, E the largest sum
+of two codes' exponents (a subnormal code has that of the smallest normal one)
+among the eight: two products of the same eight, the first 1, come out as
+1 + 2^-13 but 1 + 2^-14 as 1, and one in the next eight is kept whole.  The
+product with the largest exponent (8 bits) loses nothing, so eight products are
+off by at most 7 2^-13 2^E: `cut`, with the block's scales, below.  The rest is
+fp32: K additions, one product of scales and one FMA a block, each off by at
+most one unit of 2^-23 of the running sum of magnitudes, and one rounding to
+bf16: |got - exact| <= 2^-8 |exact| + (cut + (K + 3 blocks) 2^-23 sum |a b|)(1 + 2^-8)."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_weight_quantization_moeq_amd as moeq
+from oracle.fp8 import fp8_quantize, fp8_values
+from oracle.grouped import grouped_mm
+from tests.gpu_common import DEV, dev_bf16, host, host_bits, require_native, say
+from tests.test_gpu_grouped import ROWS, _f64, _offsets, _untouched
+from tests.test_gpu_guarded import Guarded
+
+pytestmark = pytest.mark.gpu
+BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+KINDS = {"row": (moeq.FMT_FP8_ROW, 1), "tile": (moeq.FMT_FP8_TILE, 128)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _native():
+    require_native()
+
+
+def _codes(q):
+    return host(q.qdata.view(torch.uint8))
+
+
+def _check_quantize(w, kind):
+    fmt, rows = KINDS[kind]
+    q = moeq.moeq_quantize_fp8(w, fmt)
+    codes, scales = fp8_quantize(host_bits(w).reshape(w.shape), rows)
+    assert np.array_equal(host(q.scales), scales, equal_nan=True)
+    assert np.array_equal(_codes(q), codes)
+    # and back: fp32(code * scale), rounded to bf16
+    v = fp8_values(codes, np.ones_like(scales), rows).astype(np.float32)
+    each = np.repeat(np.repeat(scales, rows, 1)[:, :w.shape[1]], 128, 2)[..., :w.shape[2]]
+    with np.errstate(all="ignore"):
+        want = torch.from_numpy(v * each).to(BF16)
+    assert torch.equal(moeq.moeq_dequantize(q).cpu().nan_to_num(1e30), want.nan_to_num(1e30))
+    return q
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("shape", [(1, 1, 16), (2, 3, 144), (1, 128, 128), (3, 130, 272), (1, 257, 2880), (5, 64, 1040)])
+def test_quantize(kind, shape):
+    say(f"fp8 quantize {kind} {shape}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w = torch.randn(shape, generator=g, device=DEV) * torch.exp2(torch.randint(-20, 20, shape[:2] + (1,), generator=g, device=DEV).float())
+    _check_quantize(w.to(BF16), kind)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("exp", [-133, -127, -120, -61, -60, -20, 0, 59, 60, 61, 110, 127])
+def test_quantize_far_from_one(kind, exp):
+    say(f"fp8 quantize {kind} 2^{exp}")
+    r = np.random.default_rng(2)
+    w = r.standard_normal((1, 130, 144)) * 0.3
+    w = torch.from_numpy(np.clip(w, -1, 1) * 1.99 * 2.0 ** exp).to(BF16)   # (a double's rounding to bf16, subnormals too)
+    assert torch.isfinite(w).all()
+    _check_quantize(w.to(DEV), kind)
+
+
+def test_every_quotient():
+    """Every significand of a block's largest value by every significand and 21
+    exponents of another: the code is the nearest of the exact quotient, so
+    that a quotient halfway between two codes goes to the even one."""
+    say("fp8 every quotient")
+    sig = np.arange(128, 256) / 128.0
+    for half in (sig[:64], sig[64:]):
+        v = half[None, None, :] * np.exp2(-np.arange(21.0))[None, :, None] * np.array([1.0, -1.0])[:, None, None]
+        w = np.zeros((128, 2 * 21, 128))
+        w[:, :, 0] = sig[:, None]
+        w[:, :, 64:] = v.reshape(1, 42, 64)
+        w = np.where(np.abs(w) > sig[:, None, None], 0.0, w)
+        w[:, :, 0] = sig[:, None]
+        _check_quantize(torch.from_numpy(w).to(BF16).to(DEV), "row")
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_zero_and_bad_blocks(kind):
+    say(f"fp8 bad blocks {kind}")
+    w = torch.randn((2, 300, 400), generator=torch.Generator().manual_seed(3))
+    w[0, :140, :130] = 0
+    w[0, 5, 5] = -0.0
+    w[0, 200, 300], w[1, 299, 399], w[1, 0, 0] = float("inf"), float("nan"), float("-inf")
+    q = _check_quantize(w.to(BF16).to(DEV), kind)
+    back = moeq.moeq_dequantize(q)
+    assert back[0, 200, 300].isnan() and back[0, 200, 299].isnan() and not back[0, 0].isnan().any()
+
+
+def _operands(sizes, before, behind, N, K, seed=0, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    off = _offsets(sizes, before)
+    M, E = int(off[-1]) + behind, len(sizes)
+    x = torch.randn((M, K), generator=g, device=DEV) * torch.exp2(torch.randint(-6, 6, (M, 1), generator=g, device=DEV).float())
+    w = torch.randn((E, N, K), generator=g, device=DEV) * scale
+    xq = moeq.moeq_quantize_fp8(x.to(BF16), moeq.FMT_FP8_ROW)
+    wq = moeq.moeq_quantize_fp8(w.to(BF16), moeq.FMT_FP8_TILE)
+    for s in (slice(0, off[0]), slice(int(off[-1]), M)):   # rows of no expert hold anything
+        xq.qdata.view(torch.uint8)[0, s] = 0x7f
+        xq.scales[0, s] = float("nan")
+    return xq, wq, off, torch.from_numpy(off).to(DEV)
+
+
+def _values(xq, wq, off):
+    xs, ws = fp8_values(_codes(xq), host(xq.scales), 1)[0], fp8_values(_codes(wq), host(wq.scales), 128)
+    xs[:off[0]] = 0
+    xs[off[-1]:] = 0
+    return xs, ws
+
+
+def _powers(q, rows):
+    """2^e of each code's exponent times the block's scale, [E, R, C] padded to eights (0 for a zero code)."""
+    v = q.qdata.float().abs()
+    p = torch.exp2(torch.floor(torch.log2(v.clamp(min=2.0 ** -6)))).double() * (v > 0)
+    s = q.scales.double().repeat_interleave(rows, 1)[:, :q.rows].repeat_interleave(128, 2)[:, :, :q.cols]
+    return p * s
+
+
+def _cut(xq, wq, off):
+    """What the instructions' alignment may take off each output, [M, N]."""
+    a, b = _powers(xq, 1)[0], _powers(wq, 128)
+    out = torch.zeros((xq.rows, wq.rows), dtype=torch.float64, device=DEV)
+    for e in range(wq.num_experts):
+        lo, hi = int(off[e]), int(off[e + 1])
+        for m in range(lo, hi, 128):
+            p = a[m:min(m + 128, hi)]
+            for k in range(0, xq.cols, 8):
+                out[m:m + p.shape[0]] += (p[:, None, k:k + 8] * b[e][None, :, k:k + 8]).amax(-1)
+    return host(7 * 2.0 ** -13 * out)
+
+
+def _check_product(y, xq, wq, off):
+    xs, ws = _values(xq, wq, off)
+    want, mag = grouped_mm(xs, ws, off), grouped_mm(np.abs(xs), np.abs(ws), off)
+    K = xq.cols
+    got = _f64(y)
+    live = ~np.isnan(want)
+    tol = 2.0 ** -8 * np.abs(want)
+    tol = tol + (_cut(xq, wq, off) + (K + 3 * -(-K // 128)) * 2.0 ** -23 * mag) * (1 + 2.0 ** -8)
+    bad = live & ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
+
+
+SHAPES = [(8, 16), (16, 128), (72, 144), (136, 272), (264, 528), (520, 1040), (1000, 400), (24, 2320)]
+
+
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("N,K", SHAPES)
+def test_product(rows, N, K):
+    say(f"fp8 product {rows} N={N} K={K}")
+    xq, wq, off, doff = _operands(*ROWS[rows], N, K)
+    y = torch.full((xq.rows, N), 7.0, dtype=BF16, device=DEV)
+    assert moeq.moeq_grouped_mm_fp8(xq, wq, doff, out=y) is y
+    _check_product(y, xq, wq, off)
+    assert _untouched(y, off)
+
+
+@pytest.mark.parametrize("sizes", [[3], [300], [2, 70, 0, 500]])
+@pytest.mark.parametrize("N,K", [(40, 8336), (264, 16400), (2600, 1040)])
+def test_long_contractions_and_many_columns(sizes, N, K):
+    say(f"fp8 product {sizes} N={N} K={K}")
+    xq, wq, off, doff = _operands(sizes, 0, 0, N, K, seed=1)
+    _check_product(moeq.moeq_grouped_mm_fp8(xq, wq, doff), xq, wq, off)
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 33, 64, 65, 96, 100, 129, 192, 200, 256, 257, 400])
+@pytest.mark.parametrize("E,N,K", [(1, 264, 1168), (40, 264, 528)])
+def test_exact_operands(M, E, N, K):
+    """Integer values with scales of powers of two: every sum is an integer
+    below 2^24 times a power of two, so the result is the exact one, rounded."""
+    say(f"fp8 exact M={M} E={E} N={N} K={K}")
+    g = torch.Generator(device=DEV).manual_seed(M)
+    rows = M * (E if E == 1 else 1)
+    off = torch.linspace(0, rows, E + 1).to(torch.int32).to(DEV)
+    xc = torch.randint(-4, 5, (1, rows, K), generator=g, device=DEV).float()
+    wc = torch.randint(-4, 5, (E, N, K), generator=g, device=DEV).float()
+    kb, nb = -(-K // 128), -(-N // 128)
+    xs = torch.exp2(torch.randint(-2, 3, (1, rows, kb), generator=g, device=DEV).float())
+    ws = torch.exp2(torch.randint(-2, 3, (E, nb, kb), generator=g, device=DEV).float())
+    xq = moeq.QWeight(moeq.FMT_FP8_ROW, 1, rows, K, xc.to(F8), xs)
+    wq = moeq.QWeight(moeq.FMT_FP8_TILE, E, N, K, wc.to(F8), ws)
+    y = moeq.moeq_grouped_mm_fp8(xq, wq, off)
+    a, b = _values(xq, wq, [0, rows])
+    want = torch.from_numpy(grouped_mm(a, b, off.tolist())).to(BF16)   # (exact in fp32 and below, then one rounding)
+    assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("M", [5, 200])
+def test_nan_blocks(M):
+    say(f"fp8 NaN blocks M={M}")
+    xq, wq, off, doff = _operands([M], 0, 0, 264, 400, seed=4)
+    xq.scales[0, 3, 2] = float("nan")
+    wq.scales[0, 1, 1] = float("nan")
+    wq.qdata.view(torch.uint8)[0, 7, 399] = 0x7f
+    y = moeq.moeq_grouped_mm_fp8(xq, wq, doff)
+    want = torch.zeros((M, 264), dtype=torch.bool)
+    want[3], want[:, 128:256], want[:, 7] = True, True, True
+    assert torch.equal(y.isnan().cpu(), want)
+
+
+GUARDED = {"one row": [1], "few": [2, 0, 9, 1, 17, 0, 3, 8], "borders": [32, 64, 65, 128, 129, 192, 193, 256, 257],
+           "many experts": [(i * 7) % 40 + 1 for i in range(300)]}
+
+
+def _guarded(w, kind):
+    fmt, _ = KINDS[kind]
+    shape = tuple(w.shape)
+    probe = moeq.QWeight(fmt, *shape, None, None)
+    q, s = (Guarded(want, dtype) for _, want, dtype in probe.layout())
+    out = moeq.QWeight(fmt, *shape, q.t, s.t)
+    moeq.moeq_quantize_fp8(w, out=out)
+    q.check("codes")
+    s.check("scales")
+    ref = moeq.moeq_quantize_fp8(w, fmt)
+    assert torch.equal(q.t.view(torch.uint8), ref.qdata.view(torch.uint8)) and torch.equal(s.t, ref.scales)
+    back = Guarded(shape, BF16)
+    assert torch.equal(moeq.moeq_dequantize(out, out=back.t), moeq.moeq_dequantize(ref))
+    back.check("read back")
+    return out
+
+
+@pytest.mark.parametrize("rows", list(GUARDED))
+@pytest.mark.parametrize("N,K", [(8, 16), (72, 144), (520, 1040)])
+def test_nothing_is_written_past_the_end(rows, N, K):
+    say(f"fp8 guarded {rows} N={N} K={K}")
+    g = torch.Generator(device=DEV).manual_seed(5)
+    off = _offsets(GUARDED[rows])
+    M, E = int(off[-1]), len(off) - 1
+    x = _guarded(torch.randn((1, M, K), generator=g, device=DEV).to(BF16), "row")
+    w = _guarded(torch.randn((E, N, K), generator=g, device=DEV).to(BF16), "tile")
+    y = Guarded((M, N), BF16)
+    doff = torch.from_numpy(off).to(DEV)
+    assert torch.equal(moeq.moeq_grouped_mm_fp8(x, w, doff, out=y.t), moeq.moeq_grouped_mm_fp8(x, w, doff))
+    y.check("out")
+
+
+@pytest.mark.parametrize("bad", [[0, 40, 20, 50], [-2 ** 31, 70, -5, 2 ** 31 - 1], [60, 0, 60, 0], [2 ** 31 - 1] * 4])
+@pytest.mark.parametrize("rows", [60, 700])
+def test_offsets_that_do_not_ascend_stay_inside(bad, rows):
+    say(f"fp8 offsets {rows} {bad}")
+    xq, wq, _, _ = _operands([rows], 0, 0, 72, 272, seed=6)
+    wq = moeq.moeq_quantize_fp8(torch.randn((3, 72, 272), device=DEV).to(BF16))
+    y = Guarded((rows, 72), BF16)
+    moeq.moeq_grouped_mm_fp8(xq, wq, torch.tensor(bad, dtype=torch.int32, device=DEV), out=y.t)
+    y.check("offsets")
+
+
+def test_one_expert_of_several():
+    """QWeight.expert: scales that start at any float."""
+    say("fp8 expert")
+    xq, wq, off, doff = _operands([4, 100, 30], 0, 0, 136, 400, seed=7)
+    y = moeq.moeq_grouped_mm_fp8(xq, wq, doff)
+    one = torch.tensor([int(off[1]), int(off[2])], dtype=torch.int32, device=DEV)
+    z = torch.zeros_like(y)
+    moeq.moeq_grouped_mm_fp8(xq, wq.expert(1), one, out=z)
+    assert torch.equal(z[off[1]:off[2]], y[off[1]:off[2]]) and not z[off[2]:].any() and not z[:off[1]].any()
+    assert torch.equal(moeq.moeq_dequantize(wq.expert(2))[0], moeq.moeq_dequantize(wq)[2])
+
+
+def test_no_rows():
+    say("fp8 no rows")
+    x = moeq.moeq_quantize_fp8(torch.empty((0, 32), dtype=BF16, device=DEV), moeq.FMT_FP8_ROW)
+    w = moeq.moeq_quantize_fp8(torch.ones((2, 8, 32), dtype=BF16, device=DEV))
+    assert moeq.moeq_grouped_mm_fp8(x, w, torch.zeros(3, dtype=torch.int32, device=DEV)).shape == (0, 8)
+    assert moeq.moeq_dequantize(x).shape == (1, 0, 32)
+
+
+def test_other_stream_and_graph():
+    say("fp8 stream, graph")
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.randn((300, 400), generator=g, device=DEV).to(BF16)
+    w = torch.randn((3, 136, 400), generator=g, device=DEV).to(BF16)
+    off = torch.tensor([0, 7, 7, 300], dtype=torch.int32, device=DEV)
+
+    def step(s=None):
+        q = moeq.moeq_quantize_fp8(w, stream=s)
+        return (moeq.moeq_grouped_mm_fp8(moeq.moeq_quantize_fp8(x, moeq.FMT_FP8_ROW, stream=s), q, off, stream=s),
+                moeq.moeq_dequantize(q, stream=s))
+
+    ref = step()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = step(s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in range(4):
+        x.copy_(torch.randn(x.shape, generator=torch.Generator(device=DEV).manual_seed(k), device=DEV))
+        ref = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref)), k
