@@ -34,6 +34,7 @@ __all__ = [
     "moeq_grouped_ffn_workspace_bytes", "moeq_grouped_ffn", "moeq_grouped_ffn_backward_workspace_bytes",
     "moeq_grouped_ffn_backward",
     "FMT_FP8_ROW", "FMT_FP8_TILE", "FP8_BLOCKSIZE", "moeq_quantize_fp8", "moeq_grouped_mm_fp8",
+    "moeq_orthogonalize_workspace_bytes", "moeq_orthogonalize",
 ]
 
 FMT_NF4 = 1
@@ -113,6 +114,8 @@ def _load():
         "moeq_grouped_mm_grad_weight": (I32, [P, P, P, I32, I32, I32, I32, I32, P, P, SZ, P]),
         "moeq_grouped_mm_grad_weight_workspace_bytes": (SZ, [I32, I32, I32, I32]),
         "moeq_grouped_mm_mxfp4": (I32, [QP, QP, P, P, P]),
+        "moeq_orthogonalize_workspace_bytes": (SZ, [I32, I32, I32]),
+        "moeq_orthogonalize": (I32, [P, I32, I32, I32, I32, P, I32, P, P, SZ, P]),
         "moeq_quantize_fp8": (I32, [P, QP, P]),
         "moeq_dequantize_fp8": (I32, [QP, P, P]),
         "moeq_grouped_mm_fp8": (I32, [QP, QP, P, P, P]),
@@ -1201,3 +1204,49 @@ def moeq_clip_grad_norm(grads, max_norm, out=None, workspace=None, stream=None):
         _check(lib.moeq_clip_grad_norm(table.buffer_info()[0], len(grads), float(max_norm), _ptr(norm), _ptr(workspace),
                                        workspace.numel(), _stream(stream, dev)), "moeq_clip_grad_norm")
     return norm
+
+
+def moeq_orthogonalize_workspace_bytes(E, N, K):
+    """Workspace bytes :func:`moeq_orthogonalize` needs (0 if the arguments are invalid)."""
+    return int(_load().moeq_orthogonalize_workspace_bytes(int(E), int(N), int(K)))
+
+
+def _coefficients(coefficients, steps):
+    """The fp32 table [steps][3] of one (a, b, c) for all steps, or of one for each."""
+    rows = list(coefficients)
+    if rows and not isinstance(rows[0], (tuple, list)):
+        rows = [rows] * steps
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError(f"coefficients must be (a, b, c), or {steps} of them")
+    return array.array("f", [float(v) for r in rows for v in r])
+
+
+def moeq_orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=None, workspace=None, stream=None):
+    """Orthogonalised update: each matrix of ``g`` (bf16 or fp32, ``[N, K]`` or a
+    batch ``[E, N, K]``) divided by its norm and taken through ``steps``
+    Newton-Schulz steps ``X <- a X + (b A + c A A) X``, ``A = X X^T``, with
+    ``coefficients`` ``(a, b, c)`` for all steps or one triple for each.  Returns
+    bf16 of ``g``'s shape.  Working matrices are fp16 with fp32 sums; a matrix of
+    zeros stays one, an infinity or a NaN makes its own matrix NaN."""
+    if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
+        raise ValueError("g must be a [N, K] or [E, N, K] tensor")
+    if g.dtype not in _GRAD_DTYPES:
+        raise TypeError(f"g must be torch.float32 or torch.bfloat16, got {g.dtype}")
+    _dev(g, g.dtype, "g")
+    if out is not None:
+        _dev(out, torch.bfloat16, "out", g.shape)
+    steps = int(steps)
+    if steps < 1:
+        raise ValueError("steps must be >= 1")
+    table = _coefficients(coefficients, steps)
+    dev = _on_device("moeq_orthogonalize", g, out)
+    o = _empty(g.shape, torch.bfloat16, dev, stream) if out is None else out
+    if g.numel() == 0:
+        return o
+    E, N, K = (1, *g.shape) if g.dim() == 2 else g.shape
+    lib = _load()
+    workspace = _workspace_for(workspace, int(lib.moeq_orthogonalize_workspace_bytes(E, N, K)), dev, stream)
+    with _current(dev):
+        _check(lib.moeq_orthogonalize(_ptr(g), _GRAD_DTYPES[g.dtype], E, N, K, table.buffer_info()[0], steps, _ptr(o),
+                                      _ptr(workspace), _numel(workspace), _stream(stream, dev)), "moeq_orthogonalize")
+    return o

@@ -20,7 +20,8 @@ LIB_NAME = "libmoeq.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.hip", "quant.hip", "route.hip", "experts.hip", "decode.hip", "router.hip",
            "api_grouped.hip", "mxfp4.hip", "grouped.hip", "clip.hip",
-           "api_ffn.hip", "ffn.hip", "api_fp8.hip", "fp8.hip", "fp8_mm.hip"]
+           "api_ffn.hip", "ffn.hip", "api_fp8.hip", "fp8.hip", "fp8_mm.hip",
+           "api_ortho.hip", "ortho.hip"]
 ARCH = "gfx950"
 
 # IEEE fp32 division and denormals stay on (no fast-math, no FTZ): the NF4 and

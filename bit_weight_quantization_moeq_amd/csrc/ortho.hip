@@ -1,0 +1,302 @@
+// Orthogonalised updates (gfx950): for each of a batch of matrices G, the
+// Newton-Schulz steps that move its singular values towards 1 and keep its
+// singular vectors,
+//
+//   X = G / |G|_F,   A = X X^T,   P = a I + b A + c A A,   X <- P X
+//
+// (A = X^T X and X <- X P where G is taller than wide, so that A has the
+// shorter side).  Three products a step, on the tile engine of
+// grouped_tile.h; the polynomial is the second one's epilogue.
+//
+// Precision.  X, A and P are kept in fp16, not in bf16: all three are bounded
+// (singular values up to about 1.2, |G|_F = 1 at the start), so fp16's range is
+// enough, its eight times smaller rounding shows in the result (Gaussian 512 x
+// 1024, five steps: 1.3e-3 off before the output's rounding, bf16 working
+// matrices 1.1e-2), and its products run at the same rate.  Powers of two keep
+// the entries in fp16's normal range: X times 2^s, s = floor(log2(sqrt(m))) with
+// m the longer side, so that entries of an orthogonal matrix are around 1, and
+// A and P times 2^8.  Sums are fp32, the norm's fp64.
+#include "grouped_tile.h"
+
+#include "ortho.h"
+
+namespace moeq {
+namespace {
+
+constexpr int kShift = 8;   // A and P are stored times 2^kShift
+constexpr int kChunk = 1 << 15;   // values per partial sum, at least
+constexpr int kMaxChunks = 64;
+
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+__device__ __forceinline__ float value(const uint16_t* p) { return bf16_value(*p); }
+__device__ __forceinline__ float value(const float* p) { return *p; }
+
+// Eight values from p on: those before `n`, zeros behind.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int64_t n, bool wide, float (&v)[8]) {
+  if (wide) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+      v[0] = lo.x; v[1] = lo.y; v[2] = lo.z; v[3] = lo.w;
+      v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
+    } else {
+      const u32x4 b = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __builtin_bit_cast(float, b[i] << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, b[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? value(p + i) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Sum of squares of chunk blockIdx.x of matrix blockIdx.y, in a fixed order.
+template <typename T>
+__global__ __launch_bounds__(256) void ortho_squares_kernel(const T* g, int64_t size, bool wide, double* partial) {
+  __shared__ double part[4];
+  const int64_t per = ((size + gridDim.x - 1) / gridDim.x + 7) / 8 * 8;
+  const int64_t lo = per * blockIdx.x, hi = min(lo + per, size);
+  const T* p = g + size * blockIdx.y;
+  double s = 0.0;
+  for (int64_t i = lo + 8 * threadIdx.x; i < hi; i += 8 * 256) {
+    float v[8];
+    load8(p + i, hi - i, wide, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
+  }
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) partial[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = part[0] + part[1] + part[2] + part[3];
+}
+
+// X = G 2^s / |G| of matrix blockIdx.y, columns padded with zeros to xc.  A
+// matrix of zeros stays one.
+template <typename T>
+__global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N, int32_t K, int32_t xc, bool wide,
+                                                          const double* partial, int32_t chunks, double times, _Float16* x) {
+  double sum = 0.0;
+  for (int i = 0; i < chunks; ++i) sum += partial[(int64_t)blockIdx.y * chunks + i];
+  const double f = sum == 0.0 ? 0.0 : times / sqrt(sum);   // (an infinity or a NaN of G: NaN or 0 times inf below)
+  const T* p = g + (int64_t)N * K * blockIdx.y;
+  _Float16* o = x + (int64_t)N * xc * blockIdx.y;
+  const uint32_t groups = xc / 8;
+  const int64_t total = (int64_t)N * groups;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)i / groups) : i / groups;
+    const int c = 8 * (int)(i - r * groups);
+    float v[8];
+    load8(p + r * K + c, K - c, wide, v);
+    f16x8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = (_Float16)(float)((double)v[j] * f);
+    *reinterpret_cast<f16x8*>(o + r * xc + c) = h;
+  }
+}
+
+// One batched product: out [rows][cols] of each matrix from the columns' operand
+// w and the rows' operand x, contraction kc.  Pitches ld* in elements (a
+// multiple of 8), matrices [strides] apart.  Which layouts w and x have, and what
+// becomes of the sums, the kernel's parameters say.
+enum class Then { kGram, kPoly, kApply, kOut };
+struct OrthoProduct {
+  const _Float16 *w, *x;
+  void* out;
+  int32_t E, rows, cols, kc, ldw, ldx, ldo;
+  int64_t sw, sx, so;
+  const _Float16* a16 = nullptr;   // kPoly: A
+  float a = 0.f, b = 0.f, c = 0.f, times = 1.f;
+};
+
+template <Then kThen, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void ortho_kernel(OrthoProduct g) {
+  using T = Tile<Op::kF16, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
+  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(4))];
+  const int nc = (g.cols + T::kCols - 1) / T::kCols, nr = (g.rows + T::kRows - 1) / T::kRows, tiles = nr * nc;
+  const int at = work_item(g.E * tiles, kTileGroup * nc);
+  if (at >= g.E * tiles) return;
+  const int e = at / tiles, q = at - e * tiles;
+  // row tiles in groups that go through the column tiles together
+  const int grp = q / (kTileGroup * nc), gt = min(kTileGroup, nr - grp * kTileGroup), rr = q - grp * kTileGroup * nc;
+  const int c0 = (rr / gt) * T::kCols, r0 = (grp * kTileGroup + rr % gt) * T::kRows;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int nrows = min(T::kRows, g.rows - r0), ncols = min(T::kCols, g.cols - c0);
+  const char* w = reinterpret_cast<const char*>(g.w + g.sw * e);
+  const char* x = reinterpret_cast<const char*>(g.x + g.sx * e);
+  typename T::A a;
+  typename T::B b;
+  const int kbytes = (g.kc + 7) / 8 * 16;   // (a row's padding is zeros)
+  if constexpr (kAT)
+    a.init(w + 2 * c0, (int64_t)g.kc * g.ldw * 2 - 2 * c0, 2 * g.ldw, 0, wave, lane);
+  else
+    a.init(w + (int64_t)c0 * g.ldw * 2, (int64_t)ncols * g.ldw * 2, 2 * g.ldw, kbytes, wave, lane);
+  if constexpr (kBT)
+    b.init(x + 2 * r0, (int64_t)g.kc * g.ldx * 2 - 2 * r0, 2 * g.ldx, 0, wave, lane);
+  else
+    b.init(x + (int64_t)r0 * g.ldx * 2, (int64_t)nrows * g.ldx * 2, 2 * g.ldx, kbytes, wave, lane);
+  f32x16 acc[kTN][kTM];
+#pragma unroll
+  for (int n = 0; n < kTN; ++n)
+#pragma unroll
+    for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
+  T::run(smem, a, b, nullptr, 0, (g.kc + 63) / 64, acc);
+
+  const _Float16* a16 = g.a16 + g.so * e;
+  const int64_t base = g.so * e;
+  // (columns up to the pitch: sums of zeros fill the padding)
+  const int width = min(T::kCols, (kThen == Then::kOut ? g.cols : g.ldo) - c0);
+  T::each8(
+      smem, acc, nrows, width,
+      [&](int r, int c) {
+        if constexpr (kThen == Then::kPoly)
+          return *reinterpret_cast<const f16x8*>(a16 + (int64_t)(r0 + r) * g.ldo + c0 + c);
+        else
+          return 0;
+      },
+      [&](int r, int c, const float (&v)[8], const auto& in) {
+        const int64_t o = base + (int64_t)(r0 + r) * g.ldo + c0 + c;
+        if constexpr (kThen == Then::kOut) {
+          uint16_t* out = static_cast<uint16_t*>(g.out) + o;
+          if (g.ldo % 8 == 0) {
+            u32x4 p;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(v[2 * i] * g.times, v[2 * i + 1] * g.times);
+            *reinterpret_cast<u32x4*>(out) = p;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (c + i < width) out[i] = (uint16_t)pack_bf16x2(v[i] * g.times, 0.f);
+          }
+        } else {
+          f16x8 h;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kThen == Then::kPoly) {
+              const float d = r0 + r == c0 + c + i ? g.a : 0.f;
+              h[i] = (_Float16)(d + (g.b * (float)in[i] + g.c * v[i]));
+            } else {
+              h[i] = (_Float16)(v[i] * g.times);
+            }
+          }
+          *reinterpret_cast<f16x8*>(static_cast<_Float16*>(g.out) + o) = h;
+        }
+      });
+}
+
+template <Then kThen, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
+hipError_t launch_shape(const OrthoProduct& g, hipStream_t s) {
+  using T = Tile<Op::kF16, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
+  const int64_t tiles = (int64_t)((g.cols + T::kCols - 1) / T::kCols) * ((g.rows + T::kRows - 1) / T::kRows);
+  ortho_kernel<kThen, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>
+      <<<(unsigned)items_grid(g.E * tiles), 64 * kNWN * kNWM, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+template <Then kThen, bool kAT, bool kBT>
+hipError_t launch_product(const OrthoProduct& g, hipStream_t s) {
+  auto tiles = [&](int size) { return (int64_t)g.E * ((g.rows + size - 1) / size) * ((g.cols + size - 1) / size); };
+  if (g.rows <= 64 || g.cols <= 64 || tiles(128) < 256) return launch_shape<kThen, kAT, kBT, 2, 2, 1, 1, 3, 3>(g, s);
+  if (tiles(256) < 256) return launch_shape<kThen, kAT, kBT, 2, 2, 2, 2, 2, 2>(g, s);
+  return launch_shape<kThen, kAT, kBT, 4, 2, 2, 4, 3, 2>(g, s);
+}
+
+int32_t pad8(int32_t n) { return (n + 7) / 8 * 8; }
+int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
+
+template <typename T>
+hipError_t launch_start(const T* g, const OrthoPlan& p, double times, double* partial, _Float16* x, hipStream_t s) {
+  const int64_t size = (int64_t)p.N * p.K;
+  const bool aligned = reinterpret_cast<uintptr_t>(g) % 16 == 0;
+  ortho_squares_kernel<T><<<dim3(p.chunks, p.E), 256, 0, s>>>(g, size, aligned && size % 8 == 0, partial);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t blocks = ((int64_t)p.N * (p.xc / 8) + 255) / 256;
+  ortho_scale_kernel<T><<<dim3((unsigned)std::min<int64_t>(blocks, 1 << 16), p.E), 256, 0, s>>>(
+      g, p.N, p.K, p.xc, aligned && p.K % 8 == 0, partial, p.chunks, times, x);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+OrthoPlan ortho_plan(int32_t E, int32_t N, int32_t K) {
+  OrthoPlan p;
+  p.E = E;
+  p.N = N;
+  p.K = K;
+  p.tall = N > K;
+  p.n = std::min(N, K);
+  p.m = std::max(N, K);
+  p.xc = pad8(K);
+  p.nc = pad8(p.n);
+  p.chunks = (int32_t)std::min<int64_t>(kMaxChunks, ((int64_t)N * K + kChunk - 1) / kChunk);
+  const int64_t x = round256((int64_t)E * N * p.xc * 2), a = round256((int64_t)E * p.n * p.nc * 2);
+  p.partial = 0;
+  p.x = round256((int64_t)E * p.chunks * 8);
+  p.y = p.x + x;
+  p.a = p.y + x;
+  p.p = p.a + a;
+  p.bytes = p.p + a;
+  return p;
+}
+
+hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p, const float* coefficients, int32_t steps,
+                                uint16_t* out, void* workspace, hipStream_t s) {
+  char* ws = static_cast<char*>(workspace);
+  double* partial = reinterpret_cast<double*>(ws + p.partial);
+  _Float16 *x = reinterpret_cast<_Float16*>(ws + p.x), *y = reinterpret_cast<_Float16*>(ws + p.y);
+  _Float16 *a = reinterpret_cast<_Float16*>(ws + p.a), *poly = reinterpret_cast<_Float16*>(ws + p.p);
+  int shift = 0;
+  while (shift < 15 && (int64_t(1) << (2 * (shift + 1))) <= p.m) ++shift;
+  const float up = (float)(1 << kShift);
+  hipError_t e = fp32 ? launch_start(static_cast<const float*>(grad), p, (double)(1 << shift), partial, x, s)
+                      : launch_start(static_cast<const uint16_t*>(grad), p, (double)(1 << shift), partial, x, s);
+  const int64_t sx = (int64_t)p.N * p.xc, sa = (int64_t)p.n * p.nc;
+  for (int i = 0; i < steps && e == hipSuccess; ++i) {
+    const float* k = coefficients + 3 * i;
+    OrthoProduct gram = {x, x, a, p.E, p.n, p.n, p.m, p.xc, p.xc, p.nc, sx, sx, sa};
+    gram.times = up / (float)(1 << shift) / (float)(1 << shift);
+    e = p.tall ? launch_product<Then::kGram, true, true>(gram, s) : launch_product<Then::kGram, false, false>(gram, s);
+    if (e != hipSuccess) break;
+    // (2^8 A)(2^8 A): A is symmetric, so its rows serve as its columns
+    OrthoProduct square = {a, a, poly, p.E, p.n, p.n, p.n, p.nc, p.nc, p.nc, sa, sa, sa};
+    square.a16 = a;
+    square.a = k[0] * up;
+    square.b = k[1];
+    square.c = k[2] / up;
+    e = launch_product<Then::kPoly, false, false>(square, s);
+    if (e != hipSuccess) break;
+    const bool last = i + 1 == steps;
+    OrthoProduct apply = {poly, x, y, p.E, p.N, p.K, p.n, p.nc, p.xc, p.xc, sa, sx, sx};   // tall: X P, P symmetric
+    if (!p.tall) {
+      apply.w = x;
+      apply.x = poly;
+      apply.ldw = p.xc;
+      apply.ldx = p.nc;
+      apply.sw = sx;
+      apply.sx = sa;
+    }
+    apply.times = 1.0f / up;
+    if (last) {
+      apply.out = out;
+      apply.ldo = p.K;
+      apply.so = (int64_t)p.N * p.K;
+      apply.times = 1.0f / up / (float)(1 << shift);
+      e = p.tall ? launch_product<Then::kOut, false, false>(apply, s) : launch_product<Then::kOut, true, false>(apply, s);
+    } else {
+      e = p.tall ? launch_product<Then::kApply, false, false>(apply, s) : launch_product<Then::kApply, true, false>(apply, s);
+      std::swap(x, y);
+    }
+  }
+  return e;
+}
+
+}  // namespace moeq

@@ -613,6 +613,30 @@ size_t moeq_clip_grad_norm_workspace_bytes(int32_t count);
 moeq_status moeq_clip_grad_norm(const moeq_grad *grads, int32_t count, double max_norm, float *norm, void *workspace,
                                 size_t workspace_bytes, void *stream);
 
+/*
+ * Orthogonalised updates, for trained expert weights: each matrix G of a batch
+ * [E][N][K] goes through `steps` Newton-Schulz steps, which move its singular
+ * values towards 1 and keep its singular vectors.  From X = G / |G| (the root of
+ * the sum of squares; a matrix of zeros stays one), step i takes
+ *   A = X X^T,   X <- a X + (b A + c A A) X,   (a, b, c) = coefficients[i]
+ *   g             bf16 (dtype MOEQ_DTYPE_BF16) or fp32 (MOEQ_DTYPE_FP32)
+ *                 [E][N][K], aligned to its type
+ *   coefficients  fp32 [steps][3] in HOST memory, read before the call returns
+ *   out_bf16      bf16 [E][N][K], 16-byte aligned
+ *   workspace     of moeq_orthogonalize_workspace_bytes(E, N, K), 16-byte aligned
+ * The norm is summed in fp64; X, A and the polynomial are kept in fp16, scaled by
+ * powers of two, with fp32 sums, and the result is rounded to bf16, so
+ * coefficients have to keep the singular values below about 2^4.  The same bits
+ * from run to run.  An infinity or a NaN makes its own matrix NaN.  MOEQ_EINVAL
+ * for buffers that overlap, coefficients that are not finite and steps outside
+ * 1..64; MOEQ_ESHAPE unless N and K are at most 2^20, the smaller at most 2^15,
+ * E <= 65535 and E (N/256 + 1)(K/256 + 1) < 2^18.
+ */
+size_t moeq_orthogonalize_workspace_bytes(int32_t E, int32_t N, int32_t K);
+moeq_status moeq_orthogonalize(const void *g, int32_t dtype, int32_t E, int32_t N, int32_t K,
+                               const float *coefficients, int32_t steps, uint16_t *out_bf16, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,7 @@ Modules:
   per 256-block group of one expert, fp32 group scales).
 * :mod:`oracle.mxfp4`   -- MXFP4 quantize, dequantize.
 * :mod:`oracle.grouped` -- products grouped by expert and their gradients.
+* :mod:`oracle.orthogonalize` -- Newton-Schulz steps on one matrix.
 * :mod:`oracle.fp8`     -- FP8 (E4M3) with a scale for each block of 128: quantize, values.
 * :mod:`oracle.ffn`     -- the gated feed-forward block over rows sorted by expert, and its gradients.
 
