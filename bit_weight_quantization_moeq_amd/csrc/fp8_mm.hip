@@ -49,74 +49,99 @@ struct Fp8Tile {
   using A = Side<false, kCols, kNW>;
   using B = Side<false, kRows, kNW>;
   static_assert(kFp8Block % (16 * kTN) == 0, "a wave's columns have one scale");
-  static_assert(kRows <= 64 * kNW, "a lane per row's scales");
+  static_assert(kRows <= 64 * (kNW - 1), "a lane per row's scales, and a wave for the weights'");
   static constexpr int kBytesB = kBufs * A::kBytes, kScales = kBytesB + kBufs * B::kBytes;
-  static constexpr int kScaleBuf = 16 * 64 * ((kRows + 63) / 64);   // a row's scales of four steps
+  // scales of four steps: the rows', then those of the weights' tiles
+  static constexpr int kScaleRows = (kRows + 63) / 64 * 64, kScaleBuf = 16 * (kScaleRows + 64);
   static constexpr int kOutPitch = 32 * kTN + 16, kPiece = 2 * 16 * kOutPitch;
   static constexpr int kLds = imax(kScales + 2 * kScaleBuf, kNW * kPiece);
   static constexpr int kInstr = A::kInstr + B::kInstr;
 
-  __device__ __forceinline__ static void frag(const char* tile, int c0, int lane, u32x4 (&f)[2]) {
-    const char* p = tile + (c0 + (lane & 15)) * kStepBytes;
-    const int swz = A::swz(lane & 15), grp = lane >> 4;
-    f[0] = *reinterpret_cast<const u32x4*>(p + 16 * (grp ^ swz));
-    f[1] = *reinterpret_cast<const u32x4*>(p + 16 * ((4 + grp) ^ swz));
+  // LDS at a bare address, so that a lane has one address for each of an
+  // operand's two halves and the rest is the instruction's offset.
+  template <typename V>
+  __device__ __forceinline__ static V lds(uint32_t at) {
+    return *(const __attribute__((address_space(3))) V*)(size_t)at;
   }
 
   __device__ __forceinline__ static void run(char* smem, const Fp8Args& g, int e, int row0, int nrows, int c0) {
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN, l16 = lane & 15, grp = lane >> 4;
     const int ncols = min(kCols, g.nout - c0), nkb = g.nkb;
-    A a;
-    B b;
-    a.init(static_cast<const char*>(g.w) + ((int64_t)e * g.nout + c0) * g.kc, (int64_t)ncols * g.kc, g.kc, g.kc, wave, lane);
-    b.init(static_cast<const char*>(g.x) + (int64_t)row0 * g.kc, (int64_t)nrows * g.kc, g.kc, g.kc, wave, lane);
+    const char* pa = static_cast<const char*>(g.w) + ((int64_t)e * g.nout + c0) * g.kc;
+    const char* pb = static_cast<const char*>(g.x) + (int64_t)row0 * g.kc;
+    const int bytes_a = ncols * g.kc, bytes_b = nrows * g.kc;
+    // (both operands have rows of kc bytes, so a lane's offsets are the same in both)
+    constexpr int kRowsAt = 8 * kNW;   // LDS rows of an instruction of all waves
+    const int at = 8 * wave + lane / 8, chunk16 = 16 * ((lane & 7) ^ A::swz(at));
+    const uint32_t voff = (uint32_t)at * (uint32_t)g.kc + (uint32_t)chunk16;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
     asm volatile("" : "+s"(lds0));  // opaque, so that it is not folded back into a pointer to the array
-    const char* xs = reinterpret_cast<const char*>(g.xs + (int64_t)row0 * nkb);
-    const int64_t xs_bytes = (int64_t)nrows * nkb * 4;
-    // the weights' scales, 64 steps at a time, one a lane
-    const int tile = min((c0 + 16 * kTN * wn) / kFp8Block, fp8_blocks(g.nout) - 1);
-    const float* ws = g.ws + ((int64_t)e * fp8_blocks(g.nout) + tile) * nkb;
-    float wsv = ws[min(lane, nkb - 1)];
+    // Scales: a wave of the first ones fetches those of 64 rows, the others all
+    // those of the tile's weights (the same bytes to the same place).
+    const bool rows_wave = 64 * wave < kRows;
+    const int tile0 = c0 / kFp8Block, tiles = fp8_blocks(g.nout);
+    const char* sp = reinterpret_cast<const char*>(rows_wave ? g.xs + (int64_t)row0 * nkb
+                                                             : g.ws + ((int64_t)e * tiles + tile0) * nkb);
+    const int64_t sp_bytes = (int64_t)(rows_wave ? nrows : tiles - tile0) * nkb * 4;
+    const uint32_t sp_off = (uint32_t)(rows_wave ? 64 * wave + lane : min(lane, tiles - tile0 - 1)) * (uint32_t)nkb * 4u;
+    const uint32_t sp_lds = lds0 + (uint32_t)(kScales + (rows_wave ? 1024 * wave : 16 * kScaleRows));
+    const int tile_row = kScaleRows + (c0 % kFp8Block + 16 * kTN * wn) / kFp8Block;
 
-    auto dma_a = [&](int ks, int i) {
-      a.template dma<false>(ks, i, wave, lds0 + (uint32_t)(ks % kBufs * A::kBytes));
+    // offset of the lane's chunk of step ks, from the step's first byte: past the end behind the row's
+    auto step_off = [&](int ks) { return ks * kStepBytes + chunk16 < g.kc ? voff : kPast; };
+    auto copy = [&](const char* p, int bytes, int ks, int i, uint32_t off, int lds) {
+      const int64_t skip = (int64_t)i * kRowsAt * g.kc + (int64_t)ks * kStepBytes;
+      dma16<false>(p + skip, bytes - skip, off, lds0 + (uint32_t)(lds + (i * kNW + wave) * 1024));
     };
-    auto dma_b = [&](int ks, int i) {
-      b.template dma<false>(ks, i, wave, lds0 + (uint32_t)(kBytesB + ks % kBufs * B::kBytes));
-    };
+    auto dma_a = [&](int ks, int buf, int i, uint32_t off) { copy(pa, bytes_a, ks, i, off, buf * A::kBytes); };
+    auto dma_b = [&](int ks, int buf, int i, uint32_t off) { copy(pb, bytes_b, ks, i, off, kBytesB + buf * B::kBytes); };
     // scales of steps 4 q .. + 3 (what lies behind a row's last one is not used)
     auto dma_scales = [&](int q) {
-      if (64 * wave < kRows) {
-        const uint32_t off = ((uint32_t)(64 * wave + lane) * (uint32_t)nkb + 4u * (uint32_t)q) * 4u;
-        dma16<false>(xs, xs_bytes, off, lds0 + (uint32_t)(kScales + (q & 1) * kScaleBuf + 1024 * wave));
-      }
+      dma16<false>(sp, sp_bytes, sp_off + 16u * (uint32_t)q, sp_lds + (uint32_t)((q & 1) * kScaleBuf));
     };
-    auto row_scale = [&](int ks, int m) {
-      return *reinterpret_cast<const float*>(smem + kScales + ((ks >> 2) & 1) * kScaleBuf +
-                                             16 * (16 * (kTM * wm + m) + l16) + 4 * (ks & 3));
+    const int swz = A::swz(l16);
+    uint32_t half[2], scale_at = lds0 + (uint32_t)(kScales + 16 * (16 * kTM * wm + l16));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) half[k] = lds0 + (uint32_t)(l16 * kStepBytes + 16 * ((4 * k + grp) ^ swz));
+    uint32_t at_a[2], at_b[2], tile_at = lds0 + (uint32_t)(kScales + 16 * tile_row);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      at_a[k] = half[k] + (uint32_t)(16 * kTN * wn * kStepBytes);
+      at_b[k] = half[k] + (uint32_t)(kBytesB + 16 * kTM * wm * kStepBytes);
+      asm volatile("" : "+v"(at_a[k]), "+v"(at_b[k]));
+    }
+    auto frag_a = [&](int buf, int n, u32x4 (&f)[2]) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) f[k] = lds<u32x4>(at_a[k] + (uint32_t)(buf * A::kBytes + 16 * kStepBytes * n));
     };
-    auto frag_a = [&](int ks, int n, u32x4 (&f)[2]) { frag(smem + ks % kBufs * A::kBytes, 16 * (kTN * wn + n), lane, f); };
-    auto frag_b = [&](int ks, int m, u32x4 (&f)[2]) {
-      frag(smem + kBytesB + ks % kBufs * B::kBytes, 16 * (kTM * wm + m), lane, f);
+    auto frag_b = [&](int buf, int m, u32x4 (&f)[2]) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) f[k] = lds<u32x4>(at_b[k] + (uint32_t)(buf * B::kBytes + 16 * kStepBytes * m));
     };
+    // scales of the step of this phase, in the buffer of its four steps
+    auto row_scale = [&](uint32_t four, int phase, int m) { return lds<float>(scale_at + four + (uint32_t)(256 * m + 4 * phase)); };
+    auto tile_scale = [&](uint32_t four, int phase) { return lds<float>(tile_at + four + (uint32_t)(4 * phase)); };
 
     dma_scales(0);
+#pragma unroll
     for (int p = 0; p < kBufs; ++p) {
-      for (int i = 0; i < A::kInstr; ++i) dma_a(p, i);
-      for (int i = 0; i < B::kInstr; ++i) dma_b(p, i);
+      const uint32_t off = step_off(p);
+#pragma unroll
+      for (int i = 0; i < A::kInstr; ++i) dma_a(p, p, i, off);
+#pragma unroll
+      for (int i = 0; i < B::kInstr; ++i) dma_b(p, p, i, off);
     }
     __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 1) * kInstr>);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 
     // the results of the last kLate matrix instructions are on their way
-    constexpr int kLate = 2, kRing = 4, kSlots = kTN * kTM;
+    constexpr int kRing = 4, kLate = kTN < kRing ? kTN : kRing - 1, kSlots = kTN * kTM;
     static_assert(kSlots % kRing == 0 && kTN >= kLate, "a step is whole turns of the ring, and a result one block of rows late");
     f32x4 acc[kTN][kTM], part[kRing];
     u32x4 fa[kTN][2], fb[2][2];
-    float sx[2], before = 0.f, now = 0.f;   // scales of the last two blocks of rows
+    float sx[2], sw, sw_next = 0.f, before = 0.f, now = 0.f;   // (before, now: scales of the last two blocks of rows)
 #pragma unroll
     for (int n = 0; n < kTN; ++n) {
 #pragma unroll
@@ -126,14 +151,20 @@ struct Fp8Tile {
 #pragma unroll
     for (int i = 0; i < kRing; ++i) part[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
     frag_b(0, 0, fb[0]);
-    sx[0] = row_scale(0, 0);
+    sx[0] = row_scale(0, 0, 0);
+    sw = tile_scale(0, 0);
     static_assert(kTM % 2 == 0, "operands in two turns");
     // Step ks: a result is added kLate matrix instructions later.  The barrier stands before the last block of rows:
     // by then every wave has the step's operands in registers, so that the
     // next step's are read, and its buffers filled anew, from there on.
-    for (int ks = 0; ks < nkb; ++ks) {
-      if (ks != 0 && (ks & 63) == 0) wsv = ws[min(ks + lane, nkb - 1)];
-      const float sw = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsv), ks & 63));
+    // (No branch inside a step: results would be moved behind it.)
+    int buf = 0;   // step ks's buffer, where the phase does not say
+    auto step = [&](auto phase, int ks) {   // phase: ks & 3
+      constexpr int kPhase = decltype(phase)::value;
+      const int here = kBufs == 2 ? kPhase & 1 : buf, next = kBufs == 2 ? here ^ 1 : here + 1 == kBufs ? 0 : here + 1;
+      const uint32_t off = step_off(ks + kBufs);
+      const uint32_t four = (uint32_t)((ks >> 2) & 1) * (uint32_t)kScaleBuf;
+      const uint32_t four_next = kPhase == 3 ? (uint32_t)kScaleBuf - four : four;
 #pragma unroll
       for (int m = 0; m < kTM; ++m) {
         const bool last = m + 1 == kTM;
@@ -141,7 +172,7 @@ struct Fp8Tile {
           __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 2) * kInstr>);
           __builtin_amdgcn_s_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-          if ((ks & 3) == 0) dma_scales((ks >> 2) + 1);
+          if constexpr (kPhase == 0) dma_scales((ks >> 2) + 1);
         }
         before = now;
         now = sx[m & 1] * sw;
@@ -156,22 +187,35 @@ struct Fp8Tile {
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(r[i], scale, s[i]);
           if (n == 0) {
-            frag_b(last ? ks + 1 : ks, (m + 1) % kTM, fb[(m + 1) & 1]);
-            sx[(m + 1) & 1] = row_scale(last ? ks + 1 : ks, (m + 1) % kTM);
+            frag_b(last ? next : here, (m + 1) % kTM, fb[(m + 1) & 1]);
+            sx[(m + 1) & 1] = last ? row_scale(four_next, (kPhase + 1) & 3, 0) : row_scale(four, kPhase, m + 1);
+            if (last) sw_next = tile_scale(four_next, (kPhase + 1) & 3);
           }
           if (last) {
-            frag_a(ks + 1, n, fa[n]);
+            frag_a(next, n, fa[n]);
 #pragma unroll
             for (int i = 0; i < A::kInstr; ++i)
-              if (i * kTN / A::kInstr == n) dma_a(ks + kBufs, i);
+              if (i * kTN / A::kInstr == n) dma_a(ks + kBufs, here, i, off);
 #pragma unroll
             for (int i = 0; i < B::kInstr; ++i)
-              if (i * kTN / B::kInstr == n) dma_b(ks + kBufs, i);
+              if (i * kTN / B::kInstr == n) dma_b(ks + kBufs, here, i, off);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      sw = sw_next;
+      buf = next;
+    };
+    int ks = 0;
+    for (; ks + 3 < nkb; ks += 4) {
+      step(std::integral_constant<int, 0>{}, ks);
+      step(std::integral_constant<int, 1>{}, ks + 1);
+      step(std::integral_constant<int, 2>{}, ks + 2);
+      step(std::integral_constant<int, 3>{}, ks + 3);
     }
+    if (ks < nkb) step(std::integral_constant<int, 0>{}, ks);
+    if (ks + 1 < nkb) step(std::integral_constant<int, 1>{}, ks + 1);
+    if (ks + 2 < nkb) step(std::integral_constant<int, 2>{}, ks + 2);
 #pragma unroll
     for (int slot = kSlots - kLate; slot < kSlots; ++slot) {
       f32x4& r = part[slot % kRing];
