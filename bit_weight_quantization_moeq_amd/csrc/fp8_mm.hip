@@ -42,6 +42,32 @@ __device__ __forceinline__ f32x4 mfma_fp8(const u32x4 (&a)[2], const u32x4 (&b)[
                                                           0x7f7f7f7f);
 }
 
+// An operand from a step's first byte on, in scalar registers: a step's copies
+// differ in the lanes' offset by a scalar, so that the loop has next to no scalar
+// arithmetic on addresses, which would hold the wave up.
+struct Rest {
+  uint32_t lo, hi;
+  int32_t left;
+  __device__ __forceinline__ Rest(const char* p, int32_t bytes)
+      : lo(__builtin_amdgcn_readfirstlane((int)(uint32_t)(uint64_t)p)),
+        hi(__builtin_amdgcn_readfirstlane((int)((uint32_t)((uint64_t)p >> 32) & 0xffffu))),
+        left(__builtin_amdgcn_readfirstlane(bytes)) {}
+  __device__ __forceinline__ void advance() {
+    const uint64_t p = ((uint64_t)hi << 32 | lo) + kStepBytes;
+    lo = (uint32_t)p;
+    hi = (uint32_t)(p >> 32);
+    left = left > kStepBytes ? left - kStepBytes : 0;
+  }
+  // 16 bytes per lane at byte off into LDS at to + 16 * lane, as dma16
+  template <typename Off>
+  __device__ __forceinline__ void copy(Off off, uint32_t to) const {
+    const u32x4 r = {(uint32_t)__builtin_amdgcn_readfirstlane((int)lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)hi),
+                     (uint32_t)__builtin_amdgcn_readfirstlane(left), 0x00020000u};
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r)
+                 : "memory", "m0");
+  }
+};
+
 // kNWN x kNWM waves, each kTN blocks of 16 columns by kTM blocks of 16 rows.
 template <int kNWN, int kNWM, int kTN, int kTM, int kBufs>
 struct Fp8Tile {
@@ -50,6 +76,11 @@ struct Fp8Tile {
   using B = Side<false, kRows, kNW>;
   static_assert(kFp8Block % (16 * kTN) == 0, "a wave's columns have one scale");
   static_assert(kRows <= 64 * (kNW - 1), "a lane per row's scales, and a wave for the weights'");
+  // The rows' buffer holds the first kHalf blocks of the waves' rows, then the
+  // others, each part in whole instructions of 64 rows.
+  static constexpr int kHalf = kTM == 2 ? 0 : kTM == 8 ? 4 : 2;
+  static_assert(kNW == 8 && kNWM == 2 && (kTM == 2 || kTM == 4 || kTM == 6 || kTM == 8), "parts of 32 or 64 rows a wave");
+  static constexpr int kInstrB1 = kHalf / 2, kInstrB2 = B::kInstr - kInstrB1;
   static constexpr int kBytesB = kBufs * A::kBytes, kScales = kBytesB + kBufs * B::kBytes;
   // scales of four steps: the rows', then those of the weights' tiles
   static constexpr int kScaleRows = (kRows + 63) / 64 * 64, kScaleBuf = 16 * (kScaleRows + 64);
@@ -72,7 +103,6 @@ struct Fp8Tile {
     const char* pb = static_cast<const char*>(g.x) + (int64_t)row0 * g.kc;
     const int bytes_a = ncols * g.kc, bytes_b = nrows * g.kc;
     // (both operands have rows of kc bytes, so a lane's offsets are the same in both)
-    constexpr int kRowsAt = 8 * kNW;   // LDS rows of an instruction of all waves
     const int at = 8 * wave + lane / 8, chunk16 = 16 * ((lane & 7) ^ A::swz(at));
     const uint32_t voff = (uint32_t)at * (uint32_t)g.kc + (uint32_t)chunk16;
     uint32_t lds0 = (uint32_t)(size_t)(__attribute__((address_space(3))) char*)smem;
@@ -88,14 +118,20 @@ struct Fp8Tile {
     const uint32_t sp_lds = lds0 + (uint32_t)(kScales + (rows_wave ? 1024 * wave : 16 * kScaleRows));
     const int tile_row = kScaleRows + (c0 % kFp8Block + 16 * kTN * wn) / kFp8Block;
 
-    // offset of the lane's chunk of step ks, from the step's first byte: past the end behind the row's
+    Rest ra(pa, bytes_a), rb(pb, bytes_b), rb2(pb, bytes_b);
+    // offset of the lane's chunk of step ks, past every end behind the row's
     auto step_off = [&](int ks) { return ks * kStepBytes + chunk16 < g.kc ? voff : kPast; };
-    auto copy = [&](const char* p, int bytes, int ks, int i, uint32_t off, int lds) {
-      const int64_t skip = (int64_t)i * kRowsAt * g.kc + (int64_t)ks * kStepBytes;
-      dma16<false>(p + skip, bytes - skip, off, lds0 + (uint32_t)(lds + (i * kNW + wave) * 1024));
+    const uint32_t lds_wave = lds0 + (uint32_t)(1024 * wave), kc = (uint32_t)g.kc;
+    auto dma_a = [&](int buf, int i, uint32_t off) {
+      ra.copy(off + (uint32_t)(8 * kNW * i) * kc, lds_wave + (uint32_t)(buf * A::kBytes + i * kNW * 1024));
     };
-    auto dma_a = [&](int ks, int buf, int i, uint32_t off) { copy(pa, bytes_a, ks, i, off, buf * A::kBytes); };
-    auto dma_b = [&](int ks, int buf, int i, uint32_t off) { copy(pb, bytes_b, ks, i, off, kBytesB + buf * B::kBytes); };
+    // instruction i of the rows' first (0) or second part
+    const uint32_t other = wave >= kNW / 2 ? (uint32_t)(16 * kTM - 32) * kc : 0u;   // parts of 32 rows: the second waves' rows
+    auto dma_b = [&](const Rest& r, int buf, int part, int i, uint32_t off) {
+      const int blocks = part ? kTM - kHalf : kHalf, row = part ? 16 * kHalf : 0;   // of a wave's rows
+      r.copy(off + (uint32_t)(row + (blocks == 4 ? i * 16 * kTM : 0)) * kc + (blocks == 4 ? 0u : other),
+             lds_wave + (uint32_t)(kBytesB + buf * B::kBytes + (part * kInstrB1 + i) * kNW * 1024));
+    };
     // scales of steps 4 q .. + 3 (what lies behind a row's last one is not used)
     auto dma_scales = [&](int q) {
       dma16<false>(sp, sp_bytes, sp_off + 16u * (uint32_t)q, sp_lds + (uint32_t)((q & 1) * kScaleBuf));
@@ -104,12 +140,15 @@ struct Fp8Tile {
     uint32_t half[2], scale_at = lds0 + (uint32_t)(kScales + 16 * (16 * kTM * wm + l16));
 #pragma unroll
     for (int k = 0; k < 2; ++k) half[k] = lds0 + (uint32_t)(l16 * kStepBytes + 16 * ((4 * k + grp) ^ swz));
-    uint32_t at_a[2], at_b[2], tile_at = lds0 + (uint32_t)(kScales + 16 * tile_row);
+    uint32_t at_a[2], at_b[2], at_b2[2], tile_at = lds0 + (uint32_t)(kScales + 16 * tile_row);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       at_a[k] = half[k] + (uint32_t)(16 * kTN * wn * kStepBytes);
-      at_b[k] = half[k] + (uint32_t)(kBytesB + 16 * kTM * wm * kStepBytes);
+      at_b[k] = half[k] + (uint32_t)(kBytesB + 16 * kHalf * wm * kStepBytes);
+      at_b2[k] = half[k] + (uint32_t)(kBytesB + (16 * kHalf * kNWM + 16 * (kTM - kHalf) * wm) * kStepBytes);
       asm volatile("" : "+v"(at_a[k]), "+v"(at_b[k]));
+      if constexpr (2 * kHalf == kTM)
+        at_b2[k] = at_b[k] + (uint32_t)(16 * kHalf * kNWM * kStepBytes);   // (a constant further)
     }
     auto frag_a = [&](int buf, int n, u32x4 (&f)[2]) {
 #pragma unroll
@@ -117,7 +156,9 @@ struct Fp8Tile {
     };
     auto frag_b = [&](int buf, int m, u32x4 (&f)[2]) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) f[k] = lds<u32x4>(at_b[k] + (uint32_t)(buf * B::kBytes + 16 * kStepBytes * m));
+      for (int k = 0; k < 2; ++k)
+        f[k] = lds<u32x4>((m < kHalf ? at_b[k] : at_b2[k] - (uint32_t)(16 * kHalf * kStepBytes)) +
+                          (uint32_t)(buf * B::kBytes + 16 * kStepBytes * m));
     };
     // scales of the step of this phase, in the buffer of its four steps
     auto row_scale = [&](uint32_t four, int phase, int m) { return lds<float>(scale_at + four + (uint32_t)(256 * m + 4 * phase)); };
@@ -128,9 +169,15 @@ struct Fp8Tile {
     for (int p = 0; p < kBufs; ++p) {
       const uint32_t off = step_off(p);
 #pragma unroll
-      for (int i = 0; i < A::kInstr; ++i) dma_a(p, p, i, off);
+      for (int i = 0; i < A::kInstr; ++i) dma_a(p, i, off);
 #pragma unroll
-      for (int i = 0; i < B::kInstr; ++i) dma_b(p, p, i, off);
+      for (int i = 0; i < kInstrB1; ++i) dma_b(rb, p, 0, i, off);
+#pragma unroll
+      for (int i = 0; i < kInstrB2; ++i)
+        if (!kHalf || p + 1 < kBufs) dma_b(rb, p, 1, i, off);
+      ra.advance();
+      rb.advance();
+      if (p + 1 < kBufs) rb2.advance();
     }
     __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 1) * kInstr>);
     __builtin_amdgcn_s_barrier();
@@ -139,72 +186,113 @@ struct Fp8Tile {
     // the results of the last kLate matrix instructions are on their way
     constexpr int kRing = 4, kLate = kTN < kRing ? kTN : kRing - 1, kSlots = kTN * kTM;
     static_assert(kSlots % kRing == 0 && kTN >= kLate, "a step is whole turns of the ring, and a result one block of rows late");
+    // Operands are read kAhead blocks of rows ahead, so that LDS, which is busy
+    // as long as the matrix cores, is never far behind; the first kPre of the
+    // columns' of the next step into registers of their own, one block after the
+    // other, the rest in the last block, each behind its last use.
+    constexpr int kAhead = kTM > 2 ? 2 : 1, kPre = kTM > 2 ? 2 : 0;
     f32x4 acc[kTN][kTM], part[kRing];
-    u32x4 fa[kTN][2], fb[2][2];
-    float sx[2], sw, sw_next = 0.f, before = 0.f, now = 0.f;   // (before, now: scales of the last two blocks of rows)
+    u32x4 fa[2][kTN][2], fb[4][2];   // (fa: the first kPre in turn, of the others only [0])
+    float sx[4], sw, sw_next = 0.f, before = 0.f, now = 0.f;   // (before, now: scales of the last two blocks of rows)
 #pragma unroll
     for (int n = 0; n < kTN; ++n) {
 #pragma unroll
       for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x4){0.f, 0.f, 0.f, 0.f};
-      frag_a(0, n, fa[n]);
+      frag_a(0, n, fa[0][n]);
     }
 #pragma unroll
     for (int i = 0; i < kRing; ++i) part[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    frag_b(0, 0, fb[0]);
-    sx[0] = row_scale(0, 0, 0);
+#pragma unroll
+    for (int m = 0; m < kAhead; ++m) {
+      frag_b(0, m, fb[m]);
+      sx[m] = row_scale(0, 0, m);
+    }
     sw = tile_scale(0, 0);
-    static_assert(kTM % 2 == 0, "operands in two turns");
-    // Step ks: a result is added kLate matrix instructions later.  The barrier stands before the last block of rows:
-    // by then every wave has the step's operands in registers, so that the
-    // next step's are read, and its buffers filled anew, from there on.
+    // Step ks: a result is added kLate matrix instructions later.  Two barriers.
+    // Before block kMid, every wave holds this step's columns and what it has
+    // left of the rows' first half in registers, and the last step's second
+    // half: the copies of the steps that take their places start there.  From
+    // block kEnd on the next step's operands are read.  Each barrier waits for
+    // what is read behind it, which was sent more than kBufs - 1 steps before;
+    // copies arrive in order, and those sent later stay in flight.
+    constexpr int kMid = kHalf ? kHalf - kAhead : 0, kEnd = kTM - 1 - kPre;
+    static_assert(kMid < kEnd || !kHalf, "the copies are sent before the second barrier");
+    constexpr int kFlyMid = kHalf ? (kBufs - 1) * kInstr - kInstrB2 : 63;
+    constexpr int kFlyEnd = kHalf ? (kBufs - 1) * kInstr : (kBufs - 2) * kInstr + A::kInstr;
     // (No branch inside a step: results would be moved behind it.)
     int buf = 0;   // step ks's buffer, where the phase does not say
     auto step = [&](auto phase, int ks) {   // phase: ks & 3
       constexpr int kPhase = decltype(phase)::value;
       const int here = kBufs == 2 ? kPhase & 1 : buf, next = kBufs == 2 ? here ^ 1 : here + 1 == kBufs ? 0 : here + 1;
-      const uint32_t off = step_off(ks + kBufs);
+      const int last = kBufs == 2 ? here ^ 1 : here == 0 ? kBufs - 1 : here - 1;
+      const uint32_t off = step_off(ks + kBufs), off_last = step_off(ks + kBufs - 1);
       const uint32_t four = (uint32_t)((ks >> 2) & 1) * (uint32_t)kScaleBuf;
       const uint32_t four_next = kPhase == 3 ? (uint32_t)kScaleBuf - four : four;
 #pragma unroll
       for (int m = 0; m < kTM; ++m) {
-        const bool last = m + 1 == kTM;
-        if (last) {
-          __builtin_amdgcn_s_waitcnt(kWaitLoads<(kBufs - 2) * kInstr>);
+        if (m == kMid) {
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<kFlyMid>);
           __builtin_amdgcn_s_barrier();
           __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
           if constexpr (kPhase == 0) dma_scales((ks >> 2) + 1);
         }
+        if (m == kEnd) {
+          __builtin_amdgcn_s_waitcnt(kWaitLoads<kFlyEnd>);
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+        }
+        const int turn = (kPhase * kTM + m) & 3, ahead = (kPhase * kTM + m + kAhead) & 3;
         before = now;
-        now = sx[m & 1] * sw;
+        now = sx[turn] * sw;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < kTN; ++n) {
           const int slot = m * kTN + n, due = (slot + kSlots - kLate) % kSlots;
-          part[slot % kRing] = mfma_fp8(fa[n], fb[m & 1]);
+          part[slot % kRing] = mfma_fp8(fa[n < kPre ? kPhase & 1 : 0][n], fb[turn]);
           const f32x4 r = part[due % kRing];
           f32x4& s = acc[due % kTN][due / kTN];
           const float scale = due / kTN == m ? now : before;
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(r[i], scale, s[i]);
-          if (n == 0) {
-            frag_b(last ? next : here, (m + 1) % kTM, fb[(m + 1) & 1]);
-            sx[(m + 1) & 1] = last ? row_scale(four_next, (kPhase + 1) & 3, 0) : row_scale(four, kPhase, m + 1);
-            if (last) sw_next = tile_scale(four_next, (kPhase + 1) & 3);
+          if (n == 0) frag_b(m + kAhead < kTM ? here : next, (m + kAhead) % kTM, fb[ahead]);
+          if (n == kTN / 2) {
+            sx[ahead] = m + kAhead < kTM ? row_scale(four, kPhase, m + kAhead)
+                                         : row_scale(four_next, (kPhase + 1) & 3, m + kAhead - kTM);
+            if (m == kEnd) sw_next = tile_scale(four_next, (kPhase + 1) & 3);
+            if (m >= kEnd && m - kEnd < kPre) frag_a(next, m - kEnd, fa[(kPhase + 1) & 1][m - kEnd]);
           }
-          if (last) {
-            frag_a(next, n, fa[n]);
+          if (m + 1 == kTM && n >= kPre) frag_a(next, n, fa[0][n]);
+          // the copies, over the blocks between the barriers
+          if constexpr (kHalf != 0) {
+            const int i = slot - kMid * kTN, over = (kEnd - kMid) * kTN;
 #pragma unroll
-            for (int i = 0; i < A::kInstr; ++i)
-              if (i * kTN / A::kInstr == n) dma_a(ks + kBufs, here, i, off);
+            for (int d = 0; d < kInstr; ++d)
+              if (i >= 0 && i < over && i == d * over / kInstr) {
+                if (d < kInstrB2)
+                  dma_b(rb2, last, 1, d, off_last);
+                else if (d < kInstrB2 + A::kInstr)
+                  dma_a(here, d - kInstrB2, off);
+                else
+                  dma_b(rb, here, 0, d - kInstrB2 - A::kInstr, off);
+              }
+          } else {
+            if (m == kMid)
 #pragma unroll
-            for (int i = 0; i < B::kInstr; ++i)
-              if (i * kTN / B::kInstr == n) dma_b(ks + kBufs, here, i, off);
+              for (int d = 0; d < A::kInstr; ++d)
+                if (d * kTN / A::kInstr == n) dma_a(here, d, off);
+            if (m == kEnd)
+#pragma unroll
+              for (int d = 0; d < kInstrB2; ++d)
+                if (d * kTN / kInstrB2 == n) dma_b(rb, here, 1, d, off);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       sw = sw_next;
       buf = next;
+      ra.advance();
+      rb.advance();
+      rb2.advance();
     };
     int ks = 0;
     for (; ks + 3 < nkb; ks += 4) {
