@@ -117,17 +117,53 @@ struct OrthoProduct {
   float a = 0.f, b = 0.f, c = 0.f, times = 1.f;
 };
 
+// A and P are symmetric: of those the tiles on and below the diagonal are
+// computed, and stored on both sides.
+constexpr bool symmetric(Then t) { return t == Then::kGram || t == Then::kPoly; }
+constexpr int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
+
+// Tile q of a matrix's nr x nc, row tiles in groups that go through the column
+// tiles together.
+template <bool kTriangle>
+__device__ __forceinline__ void tile_at(int q, int nr, int nc, int& rt, int& ct) {
+  if constexpr (!kTriangle) {
+    const int grp = q / (kTileGroup * nc), gt = min(kTileGroup, nr - grp * kTileGroup), rr = q - grp * kTileGroup * nc;
+    ct = rr / gt;
+    rt = grp * kTileGroup + rr % gt;
+  } else {
+    int first = 0;   // row of the group
+    while (first + kTileGroup < nr && q >= (int)triangle(first + kTileGroup)) first += kTileGroup;
+    const int gt = min(kTileGroup, nr - first);
+    int r = q - (int)triangle(first);
+    if (r < (first + 1) * gt) {   // columns that all of its rows have
+      ct = r / gt;
+      rt = first + r % gt;
+    } else {                      // then one row less each
+      r -= (first + 1) * gt;
+      int k = 1;
+      while (r >= gt - k) r -= gt - k++;
+      ct = first + k;
+      rt = ct + r;
+    }
+  }
+}
+
 template <Then kThen, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void ortho_kernel(OrthoProduct g) {
   using T = Tile<Op::kF16, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
-  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, T::out_bytes(4))];
-  const int nc = (g.cols + T::kCols - 1) / T::kCols, nr = (g.rows + T::kRows - 1) / T::kRows, tiles = nr * nc;
+  constexpr bool kMirror = symmetric(kThen);
+  static_assert(!kMirror || T::kRows == T::kCols, "square tiles");
+  // the wave's piece of LDS: 32 rows in fp32, and the same turned in fp16
+  constexpr int kPitch = 128 * kTN + 16, kTurned = 64 + 16, kPiece = 32 * kPitch + 32 * kTN * kTurned;
+  __shared__ __attribute__((aligned(16))) char smem[imax(T::kLds, kMirror ? T::kNW * kPiece : T::out_bytes(4))];
+  const int nc = (g.cols + T::kCols - 1) / T::kCols, nr = (g.rows + T::kRows - 1) / T::kRows;
+  const int tiles = kMirror ? (int)triangle(nr) : nr * nc;
   const int at = work_item(g.E * tiles, kTileGroup * nc);
   if (at >= g.E * tiles) return;
-  const int e = at / tiles, q = at - e * tiles;
-  // row tiles in groups that go through the column tiles together
-  const int grp = q / (kTileGroup * nc), gt = min(kTileGroup, nr - grp * kTileGroup), rr = q - grp * kTileGroup * nc;
-  const int c0 = (rr / gt) * T::kCols, r0 = (grp * kTileGroup + rr % gt) * T::kRows;
+  const int e = at / tiles;
+  int rt, ct;
+  tile_at<kMirror>(at - e * tiles, nr, nc, rt, ct);
+  const int c0 = ct * T::kCols, r0 = rt * T::kRows;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int nrows = min(T::kRows, g.rows - r0), ncols = min(T::kCols, g.cols - c0);
   const char* w = reinterpret_cast<const char*>(g.w + g.sw * e);
@@ -150,52 +186,99 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void ortho_kerne
     for (int m = 0; m < kTM; ++m) acc[n][m] = (f32x16){};
   T::run(smem, a, b, nullptr, 0, (g.kc + 63) / 64, acc);
 
-  const _Float16* a16 = g.a16 + g.so * e;
   const int64_t base = g.so * e;
-  // (columns up to the pitch: sums of zeros fill the padding)
-  const int width = min(T::kCols, (kThen == Then::kOut ? g.cols : g.ldo) - c0);
-  T::each8(
-      smem, acc, nrows, width,
-      [&](int r, int c) {
-        if constexpr (kThen == Then::kPoly)
-          return *reinterpret_cast<const f16x8*>(a16 + (int64_t)(r0 + r) * g.ldo + c0 + c);
-        else
-          return 0;
-      },
-      [&](int r, int c, const float (&v)[8], const auto& in) {
-        const int64_t o = base + (int64_t)(r0 + r) * g.ldo + c0 + c;
-        if constexpr (kThen == Then::kOut) {
-          uint16_t* out = static_cast<uint16_t*>(g.out) + o;
-          if (g.ldo % 8 == 0) {
-            u32x4 p;
+  if constexpr (kMirror) {
+    // Rows and columns up to the pitch: what lies behind the matrix is sums of
+    // zeros, and fills the padding.
+    const _Float16* a16 = g.a16 + base;
+    _Float16* out = static_cast<_Float16*>(g.out) + base;
+    constexpr int kLanes = 4 * kTN, kRowsAt = 64 / kLanes;
+    const int wn = wave % kNWN, wm = wave / kNWN, l32 = lane & 31, h = lane >> 5;
+    char *buf = smem + wave * kPiece, *turned = buf + 32 * kPitch;
+    const int lc = 8 * (lane % kLanes), c = c0 + 32 * kTN * wn + lc, cw = c0 + 32 * kTN * wn;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(v[2 * i] * g.times, v[2 * i + 1] * g.times);
-            *reinterpret_cast<u32x4*>(out) = p;
-          } else {
+    for (int m = 0; m < kTM; ++m) {
+      const int rw = r0 + 32 * (kTM * wm + m);
+      if (rw >= g.ldo) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c + i < width) out[i] = (uint16_t)pack_bf16x2(v[i] * g.times, 0.f);
-          }
-        } else {
-          f16x8 h;
+      for (int n = 0; n < kTN; ++n)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (kThen == Then::kPoly) {
-              const float d = r0 + r == c0 + c + i ? g.a : 0.f;
-              h[i] = (_Float16)(d + (g.b * (float)in[i] + g.c * v[i]));
-            } else {
-              h[i] = (_Float16)(v[i] * g.times);
-            }
-          }
-          *reinterpret_cast<f16x8*>(static_cast<_Float16*>(g.out) + o) = h;
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& v = acc[n][m];
+          *reinterpret_cast<float4*>(buf + l32 * kPitch + 4 * (32 * n + 8 * q + 4 * h)) =
+              make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
         }
-      });
+      // (a wave's LDS accesses are done in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < 32 / kRowsAt; ++u) {
+        const int lr = u * kRowsAt + lane / kLanes, r = rw + lr;
+        const float4 lo = *reinterpret_cast<const float4*>(buf + lr * kPitch + 4 * lc);
+        const float4 hi = *reinterpret_cast<const float4*>(buf + lr * kPitch + 4 * lc + 16);
+        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        f16x8 o;
+        if constexpr (kThen == Then::kPoly) {
+          f16x8 in = {};
+          if (r < g.rows && c < g.ldo) in = *reinterpret_cast<const f16x8*>(a16 + (int64_t)r * g.ldo + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            o[i] = (_Float16)((r == c + i && r < g.rows ? g.a : 0.f) + (g.b * (float)in[i] + g.c * v[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = (_Float16)(v[i] * g.times);
+        }
+        if (r < g.rows && c < g.ldo) *reinterpret_cast<f16x8*>(out + (int64_t)r * g.ldo + c) = o;
+        if (rt != ct)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) *reinterpret_cast<_Float16*>(turned + (lc + i) * kTurned + 2 * lr) = o[i];
+      }
+      if (rt != ct) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 2 * kTN; ++k) {
+          const int lr = 16 * k + lane / 4, r = cw + lr, cc = rw + 8 * (lane & 3);
+          const f16x8 o = *reinterpret_cast<const f16x8*>(turned + lr * kTurned + 16 * (lane & 3));
+          if (r < g.rows && cc < g.ldo) *reinterpret_cast<f16x8*>(out + (int64_t)r * g.ldo + cc) = o;
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+    }
+  } else {
+    // (columns up to the pitch: sums of zeros fill the padding)
+    const int width = min(T::kCols, (kThen == Then::kOut ? g.cols : g.ldo) - c0);
+    T::each8(
+        smem, acc, nrows, width, [](int, int) { return 0; },
+        [&](int r, int c, const float (&v)[8], int) {
+          const int64_t o = base + (int64_t)(r0 + r) * g.ldo + c0 + c;
+          if constexpr (kThen == Then::kOut) {
+            uint16_t* out = static_cast<uint16_t*>(g.out) + o;
+            if (g.ldo % 8 == 0) {
+              u32x4 p;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(v[2 * i] * g.times, v[2 * i + 1] * g.times);
+              __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(out));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (c + i < width) out[i] = (uint16_t)pack_bf16x2(v[i] * g.times, 0.f);
+            }
+          } else {
+            f16x8 h;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = (_Float16)(v[i] * g.times);
+            *reinterpret_cast<f16x8*>(static_cast<_Float16*>(g.out) + o) = h;
+          }
+        });
+  }
 }
 
 template <Then kThen, bool kAT, bool kBT, int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
 hipError_t launch_shape(const OrthoProduct& g, hipStream_t s) {
   using T = Tile<Op::kF16, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
-  const int64_t tiles = (int64_t)((g.cols + T::kCols - 1) / T::kCols) * ((g.rows + T::kRows - 1) / T::kRows);
+  const int64_t nr = (g.rows + T::kRows - 1) / T::kRows, tiles = symmetric(kThen) ? triangle(nr) : nr * ((g.cols + T::kCols - 1) / T::kCols);
   ortho_kernel<kThen, kAT, kBT, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>
       <<<(unsigned)items_grid(g.E * tiles), 64 * kNWN * kNWM, 0, s>>>(g);
   return hipGetLastError();
