@@ -32,6 +32,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+struct PackBf16 {
+  __device__ __forceinline__ uint32_t operator()(float lo, float hi) const { return pack_bf16x2(lo, hi); }
+};
+
 // s_waitcnt immediate: at most N vector-memory loads outstanding and every LDS
 // access of this wave done (gfx9 encoding: vmcnt in bits 3:0 and 15:14, expcnt
 // 6:4, lgkmcnt 11:8).
@@ -421,9 +425,10 @@ struct Tile {
   template <typename T>
   static constexpr int kOutPitch = 32 * kTN * (int)sizeof(T) + 16;
   static constexpr int kOutBufs = kTM > 1 ? 2 : 1;
-  template <typename T>
+  // Values of two bytes are made by pack, two at a time.
+  template <typename T, typename Pack = PackBf16>
   __device__ __forceinline__ static void store(char* smem, const f32x16 (&acc)[kTN][kTM], T* out, int64_t ld, int nrows,
-                                               int ncols) {
+                                               int ncols, Pack pack = Pack()) {
     constexpr int kPer = 16 / (int)sizeof(T), kLanes = 32 * kTN / kPer;   // lanes per row
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave % kNWN, wm = wave / kNWN, l32 = lane & 31, h = lane >> 5;
@@ -444,7 +449,7 @@ struct Tile {
             *reinterpret_cast<float4*>(p) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           else
             *reinterpret_cast<uint2*>(p) =
-                make_uint2(pack_bf16x2(v[4 * q], v[4 * q + 1]), pack_bf16x2(v[4 * q + 2], v[4 * q + 3]));
+                make_uint2(pack(v[4 * q], v[4 * q + 1]), pack(v[4 * q + 2], v[4 * q + 3]));
         }
       // (a wave's LDS accesses are done in order)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");

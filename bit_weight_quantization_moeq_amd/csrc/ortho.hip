@@ -87,6 +87,9 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N,
   double sum = 0.0;
   for (int i = 0; i < chunks; ++i) sum += partial[(int64_t)blockIdx.y * chunks + i];
   const double f = sum == 0.0 ? 0.0 : times / sqrt(sum);   // (an infinity or a NaN of G: NaN or 0 times inf below)
+  // in fp32 where it can hold the factor (the same to fp16's rounding), which is quicker
+  const bool narrow = f > 0x1p-100 && f < 0x1p100;
+  const float f32 = (float)f;
   const T* p = g + (int64_t)N * K * blockIdx.y;
   _Float16* o = x + (int64_t)N * xc * blockIdx.y;
   const uint32_t groups = xc / 8;
@@ -98,7 +101,7 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N,
     load8(p + r * K + c, K - c, wide, v);
     f16x8 h;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = (_Float16)(float)((double)v[j] * f);
+    for (int j = 0; j < 8; ++j) h[j] = (_Float16)(narrow ? v[j] * f32 : (float)((double)v[j] * f));
     *reinterpret_cast<f16x8*>(o + r * xc + c) = h;
   }
 }
@@ -121,6 +124,18 @@ struct OrthoProduct {
 // computed, and stored on both sides.
 constexpr bool symmetric(Then t) { return t == Then::kGram || t == Then::kPoly; }
 constexpr int64_t triangle(int64_t n) { return n * (n + 1) / 2; }
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+struct ScaledF16 {
+  float times;
+  __device__ __forceinline__ uint32_t operator()(float lo, float hi) const {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo * times, hi * times}), f16x2));
+  }
+};
+struct ScaledBf16 {
+  float times;
+  __device__ __forceinline__ uint32_t operator()(float lo, float hi) const { return pack_bf16x2(lo * times, hi * times); }
+};
 
 // Tile q of a matrix's nr x nc, row tiles in groups that go through the column
 // tiles together.
@@ -249,29 +264,19 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void ortho_kerne
   } else {
     // (columns up to the pitch: sums of zeros fill the padding)
     const int width = min(T::kCols, (kThen == Then::kOut ? g.cols : g.ldo) - c0);
-    T::each8(
-        smem, acc, nrows, width, [](int, int) { return 0; },
-        [&](int r, int c, const float (&v)[8], int) {
-          const int64_t o = base + (int64_t)(r0 + r) * g.ldo + c0 + c;
-          if constexpr (kThen == Then::kOut) {
-            uint16_t* out = static_cast<uint16_t*>(g.out) + o;
-            if (g.ldo % 8 == 0) {
-              u32x4 p;
+    uint16_t* out = static_cast<uint16_t*>(g.out) + base + (int64_t)r0 * g.ldo + c0;
+    if constexpr (kThen == Then::kApply)
+      T::store(smem, acc, out, g.ldo, nrows, width, ScaledF16{g.times});
+    else if (g.ldo % 8 == 0)
+      T::store(smem, acc, out, g.ldo, nrows, width, ScaledBf16{g.times});
+    else
+      T::each8(
+          smem, acc, nrows, width, [](int, int) { return 0; },
+          [&](int r, int c, const float (&v)[8], int) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(v[2 * i] * g.times, v[2 * i + 1] * g.times);
-              __builtin_nontemporal_store(p, reinterpret_cast<u32x4*>(out));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (c + i < width) out[i] = (uint16_t)pack_bf16x2(v[i] * g.times, 0.f);
-            }
-          } else {
-            f16x8 h;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = (_Float16)(v[i] * g.times);
-            *reinterpret_cast<f16x8*>(static_cast<_Float16*>(g.out) + o) = h;
-          }
-        });
+            for (int i = 0; i < 8; ++i)
+              if (c + i < width) out[(int64_t)r * g.ldo + c + i] = (uint16_t)pack_bf16x2(v[i] * g.times, 0.f);
+          });
   }
 }
 
