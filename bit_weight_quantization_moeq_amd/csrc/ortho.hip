@@ -297,6 +297,243 @@ hipError_t launch_product(const OrthoProduct& g, hipStream_t s) {
   return launch_shape<kThen, kAT, kBT, 4, 2, 2, 4, 3, 2>(g, s);
 }
 
+// ---------------------------------------------------------------------------
+// Few rows (adapters): one workgroup takes a matrix through all steps.  X stays
+// in registers, in blocks of 16 x 16 as v_mfma_f32_16x16x16_f16 leaves its result
+// (lane (c, g): rows 4 g .. + 3 of column c), which is also the layout of its
+// second operand, and of its first for a symmetric matrix.  So A A, the polynomial
+// and X <- P X need no exchange; A = X X^T sums over columns, for which a block is
+// turned on its way through the wave's own piece of LDS (written in columns, read
+// with ds_read_b64_tr_b16), and the waves' sums are added through LDS.  One launch
+// instead of three a step: 64 matrices of [16, 2048] 124 us in tiles, 21 us here (1024 of them 769 and 68; 64 of [32, 4096] 218 and 87).
+// ---------------------------------------------------------------------------
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+struct OrthoSteps {
+  float abc[kOrthoMaxSteps][3];
+};
+constexpr int kBatch = 4;
+
+// kNW waves; kNB blocks of 16 rows, kCB of 16 columns a wave.
+template <typename T, bool kTall, int kNW, int kNB, int kCB>
+__global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t n, int32_t m, bool wide, int32_t steps,
+                                                                   OrthoSteps table, float scale, uint16_t* out) {
+  __shared__ __attribute__((aligned(16))) char turn[kNW][kBatch * kNB * 512];
+  __shared__ __attribute__((aligned(16))) f32x4 part[kNW][kNB * kNB][64];
+  __shared__ double sums[kNW];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), l16 = lane & 15, grp = lane >> 4;
+  const int64_t size = (int64_t)n * m;
+  g += size * blockIdx.x;
+  out += size * blockIdx.x;
+
+  double s = 0.0;
+  for (int64_t i = 8 * t; i < size; i += 8 * 64 * kNW) {
+    float v[8];
+    load8(g + i, size - i, wide, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += (double)v[j] * (double)v[j];
+  }
+  s = wave_sum(s);
+  if (lane == 0) sums[wave] = s;
+  __syncthreads();
+  double sum = 0.0;
+  for (int i = 0; i < kNW; ++i) sum += sums[i];
+  const double f = sum == 0.0 ? 0.0 : (double)scale / sqrt(sum);
+
+  // element (r, c) of X is at r m + c of a wide matrix and at c n + r of a tall one
+  const bool four = wide && n % 4 == 0;   // a lane's four rows of a tall matrix are one access
+  auto column = [&](int b) { return 16 * (kNW * b + wave) + l16; };
+  const bool narrow = f > 0x1p-100 && f < 0x1p100;   // (as ortho_scale_kernel)
+  const float f32 = (float)f;
+  const __amdgpu_buffer_rsrc_t from = buffer(reinterpret_cast<const char*>(g), size * (int64_t)sizeof(T));
+  f16x4 x[kNB][kCB];
+#pragma unroll
+  for (int b = 0; b < kCB; ++b) {
+    const int c = column(b);
+#pragma unroll
+    for (int i = 0; i < kNB; ++i) {
+      float v[4];
+      if (kTall && four) {
+        const int r = 16 * i + 4 * grp, off = (int)(r < n && c < m ? sizeof(T) * (uint32_t)(c * n + r) : kPast);
+        if constexpr (sizeof(T) == 2) {
+          const auto q = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(from, off, 0, 0));
+          v[0] = __builtin_bit_cast(float, q.x << 16);
+          v[1] = __builtin_bit_cast(float, q.x & 0xffff0000u);
+          v[2] = __builtin_bit_cast(float, q.y << 16);
+          v[3] = __builtin_bit_cast(float, q.y & 0xffff0000u);
+        } else {
+          const u32x4 q = buffer_load16(from, (uint32_t)off);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, q[j]);
+        }
+      } else
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = 16 * i + 4 * grp + j;
+        const uint32_t at = sizeof(T) * (kTall ? (uint32_t)(c * n + r) : (uint32_t)(r * m + c));
+        const int off = (int)(r < n && c < m ? at : kPast);   // (past the end: 0)
+        if constexpr (sizeof(T) == 2)
+          v[j] = bf16_value((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, off, 0, 0));
+        else
+          v[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, off, 0, 0));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[i][b][j] = (_Float16)(narrow ? v[j] * f32 : (float)((double)v[j] * f));
+      asm volatile("" : "+v"(x[i][b]));   // (in two registers from here on)
+    }
+    if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // (all loads at once would not fit the registers)
+  }
+  const float up = (float)(1 << kShift), down = 1.0f / up, gram_times = up / scale / scale;
+  char* mine = turn[wave];
+  f16x4 p16[kNB][kNB];
+  // P X of column block b
+  auto apply = [&](int b, f32x4 (&y)[kNB]) {
+#pragma unroll
+    for (int i = 0; i < kNB; ++i) {
+      y[i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < kNB; ++q) y[i] = __builtin_amdgcn_mfma_f32_16x16x16f16(p16[q][i], x[q][b], y[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kNB; ++i) mfma_done(y[i]);
+  };
+  for (int k = 0;; ++k) {
+    f32x4 a[kNB][kNB];
+#pragma unroll
+    for (int i = 0; i < kNB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) a[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int b0 = 0; b0 < kCB; b0 += kBatch) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+          *reinterpret_cast<f16x4*>(mine + (b * kNB + i) * 512 + 32 * l16 + 8 * grp) = x[i][b0 + b];
+      // (a wave's LDS accesses are done in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        f16x4 rows[kNB];
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+          rows[i] = __builtin_bit_cast(f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                  (lds_v4i16*)(mine + (b * kNB + i) * 512 + 8 * lane)));
+#pragma unroll
+        for (int i = 0; i < kNB; ++i)
+#pragma unroll
+          for (int j = 0; j < kNB; ++j)
+            a[i][j] = __builtin_amdgcn_mfma_f32_16x16x16f16(rows[i], rows[j], a[i][j], 0, 0, 0);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kNB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        mfma_done(a[i][j]);
+        part[wave][i * kNB + j][lane] = a[i][j];
+      }
+    __syncthreads();
+    f16x4 a16[kNB][kNB];
+#pragma unroll
+    for (int i = 0; i < kNB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        f32x4 v = part[0][i * kNB + j][lane];
+#pragma unroll 5
+        for (int w = 1; w < kNW; ++w) {
+          const f32x4 q = part[w][i * kNB + j][lane];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) v[z] += q[z];
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) a16[i][j][z] = (_Float16)(v[z] * gram_times);
+      }
+    __syncthreads();   // (before the next step's sums)
+    // (2^8 A)(2^8 A): a symmetric matrix's block (k, i) is the first operand's (i, k)
+    const float ca = table.abc[k][0] * up, cb = table.abc[k][1], cc = table.abc[k][2] * down;
+#pragma unroll
+    for (int i = 0; i < kNB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < kNB; ++q) v = __builtin_amdgcn_mfma_f32_16x16x16f16(a16[q][i], a16[q][j], v, 0, 0, 0);
+        mfma_done(v);
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          p16[i][j][z] = (_Float16)((i == j && 4 * grp + z == l16 ? ca : 0.f) + (cb * (float)a16[i][j][z] + cc * v[z]));
+      }
+    if (k + 1 >= steps) break;
+#pragma unroll
+    for (int b = 0; b < kCB; ++b) {   // (blocks behind the last are zeros, and stay so)
+      f32x4 y[kNB];
+      apply(b, y);
+#pragma unroll
+      for (int i = 0; i < kNB; ++i)
+#pragma unroll
+        for (int z = 0; z < 4; ++z) x[i][b][z] = (_Float16)(y[i][z] * down);
+#pragma unroll
+      for (int i = 0; i < kNB; ++i) asm volatile("" : "+v"(x[i][b]));
+      if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // (addresses made anew, not kept from the loads through all steps)
+  const __amdgpu_buffer_rsrc_t to = buffer(reinterpret_cast<const char*>(out), size * 2);
+  const float last = down / scale;
+  int c0 = 16 * wave + l16, r0 = 4 * grp;
+  asm volatile("" : "+v"(c0), "+v"(r0));
+#pragma unroll
+  for (int b = 0; b < kCB; ++b) {
+    f32x4 y[kNB];
+    apply(b, y);
+    const int c = c0 + 16 * kNW * b;
+#pragma unroll
+    for (int i = 0; i < kNB; ++i)
+      if (kTall && four) {
+        const int r = 16 * i + r0, off = (int)(r < n && c < m ? 2u * (uint32_t)(c * n + r) : kPast);
+        const uint2 q = make_uint2(pack_bf16x2(y[i][0] * last, y[i][1] * last), pack_bf16x2(y[i][2] * last, y[i][3] * last));
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, q), to, off, 0, 0);
+      } else
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const int r = 16 * i + r0 + z;
+        const uint32_t at = 2u * (kTall ? (uint32_t)(c * n + r) : (uint32_t)(r * m + c));
+        __builtin_amdgcn_raw_buffer_store_b16((short)pack_bf16x2(y[i][z] * last, 0.f), to, (int)(r < n && c < m ? at : kPast), 0,
+                                              0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Whether a matrix fits a workgroup's registers: up to 16 waves of 8 column
+// blocks, or 8 waves, which have twice the registers, of 64 (for two row blocks 32).
+bool few(const OrthoPlan& p) { return p.n <= 32 && p.m <= (p.n <= 16 ? 8192 : 4096); }
+
+template <typename T, bool kTall>
+hipError_t launch_few(const T* g, const OrthoPlan& p, const OrthoSteps& table, int32_t steps, float scale, uint16_t* out,
+                      hipStream_t s) {
+  const bool wide = reinterpret_cast<uintptr_t>(g) % 16 == 0 && (int64_t)p.n * p.m % 8 == 0;
+  auto go = [&](auto kernel, int waves) {
+    kernel<<<(unsigned)p.E, 64 * waves, 0, s>>>(g, p.n, p.m, wide, steps, table, scale, out);
+  };
+  if (p.n <= 16 && p.m <= 2048)
+    go(ortho_few_kernel<T, kTall, 16, 1, 8>, 16);
+  else if (p.n <= 16)
+    go(ortho_few_kernel<T, kTall, 8, 1, 64>, 8);
+  else if (p.m <= 2048)
+    go(ortho_few_kernel<T, kTall, 16, 2, 8>, 16);
+  else
+    go(ortho_few_kernel<T, kTall, 8, 2, 32>, 8);
+  return hipGetLastError();
+}
+
 int32_t pad8(int32_t n) { return (n + 7) / 8 * 8; }
 int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
 
@@ -338,12 +575,24 @@ OrthoPlan ortho_plan(int32_t E, int32_t N, int32_t K) {
 
 hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p, const float* coefficients, int32_t steps,
                                 uint16_t* out, void* workspace, hipStream_t s) {
+  int shift = 0;
+  while (shift < 15 && (int64_t(1) << (2 * (shift + 1))) <= p.m) ++shift;
+  if (few(p)) {
+    OrthoSteps table = {};
+    for (int i = 0; i < 3 * steps; ++i) table.abc[i / 3][i % 3] = coefficients[i];
+    const float scale = (float)(1 << shift);
+    const uint16_t* g16 = static_cast<const uint16_t*>(grad);
+    const float* g32 = static_cast<const float*>(grad);
+    if (p.tall)
+      return fp32 ? launch_few<float, true>(g32, p, table, steps, scale, out, s)
+                  : launch_few<uint16_t, true>(g16, p, table, steps, scale, out, s);
+    return fp32 ? launch_few<float, false>(g32, p, table, steps, scale, out, s)
+                : launch_few<uint16_t, false>(g16, p, table, steps, scale, out, s);
+  }
   char* ws = static_cast<char*>(workspace);
   double* partial = reinterpret_cast<double*>(ws + p.partial);
   _Float16 *x = reinterpret_cast<_Float16*>(ws + p.x), *y = reinterpret_cast<_Float16*>(ws + p.y);
   _Float16 *a = reinterpret_cast<_Float16*>(ws + p.a), *poly = reinterpret_cast<_Float16*>(ws + p.p);
-  int shift = 0;
-  while (shift < 15 && (int64_t(1) << (2 * (shift + 1))) <= p.m) ++shift;
   const float up = (float)(1 << kShift);
   hipError_t e = fp32 ? launch_start(static_cast<const float*>(grad), p, (double)(1 << shift), partial, x, s)
                       : launch_start(static_cast<const uint16_t*>(grad), p, (double)(1 << shift), partial, x, s);

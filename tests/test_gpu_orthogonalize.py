@@ -198,3 +198,18 @@ def test_oracle_side():
     """(the bound's exact result is the oracle's)"""
     g = np.random.default_rng(10).standard_normal((12, 7))
     assert np.allclose(_bound(g, (COEFFICIENTS,) * 5)[1], orthogonalize(g), atol=1e-12)
+
+
+# (rows up to 16 and up to 32, either side long, columns up to 2048 and beyond, and what is past them)
+@pytest.mark.parametrize("shape", [(2, 16, 2049), (2, 2500, 9), (1, 16, 8192), (1, 8192, 16), (1, 13, 8193), (3, 17, 2048),
+                                   (2, 32, 2049), (1, 4096, 32), (1, 4097, 31), (300, 7, 130), (2, 33, 2048)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_rows(shape, dtype):
+    say(f"orthogonalize few rows {shape} {dtype}")
+    g = torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(11), device=DEV).to(dtype)
+    out = Guarded(shape, BF16)
+    moeq.moeq_orthogonalize(g, out=out.t)
+    out.check("out")
+    pick = [0, shape[0] - 1]
+    _check(g[pick], out.t[pick])
+    assert torch.equal(out.t, moeq.moeq_orthogonalize(g))
