@@ -197,6 +197,127 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_backwar
   glu_backward_tile<kNWN, kNWM, kTN, 1, kBufsA, kBufsB>(smem, g, gu, dgu, e, row0, nrows, c0);
 }
 
+// Few rows per expert (decode): gate and up columns stream past at most 16 rows
+// straight into the matrix instructions' operands, as in the other products'
+// form: 16 columns of h a work item, a unit of 256 B of their two weight rows
+// and of the token rows at a time, one unit ahead.
+constexpr int kUnitBytes = 256, kFewWaves = 4;
+
+template <bool kSplit>
+__global__ __launch_bounds__(64 * kFewWaves) void glu_few_rows_kernel(GroupedArgs g, uint16_t* gu) {
+  constexpr int kCols = kSplit ? 16 : 16 * kFewWaves;   // of a workgroup
+  __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][2][64];
+  int e, row0, nrows, ct;
+  if (!find_tile(g, 16, (g.nout + kCols - 1) / kCols, e, row0, nrows, ct)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, grp = lane >> 4, kbytes = 2 * g.kc, I = g.nout;
+  const int c0 = ct * kCols + (kSplit ? 0 : 16 * wave), ncols = min(16, I - c0);
+  if (!kSplit && ncols <= 0) return;   // (no barrier there)
+  const __amdgpu_buffer_rsrc_t rx = buffer(static_cast<const char*>(g.x) + (int64_t)row0 * kbytes, (int64_t)nrows * kbytes);
+  const char* w = static_cast<const char*>(g.w) + ((int64_t)e * 2 * I + c0) * kbytes;
+  const __amdgpu_buffer_rsrc_t rw[2] = {buffer(w, (int64_t)ncols * kbytes),
+                                        buffer(w + (int64_t)I * kbytes, (int64_t)ncols * kbytes)};
+  struct Unit {
+    u32x4 w[2][4], x[4];
+  };
+  // unit u (what is out of range loads zeros)
+  auto load = [&](Unit& v, int u) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = u * kUnitBytes + 64 * j + 16 * grp;
+      const uint32_t off = at < kbytes ? (uint32_t)l16 * (uint32_t)kbytes + (uint32_t)at : kPast;
+      v.w[0][j] = buffer_load16(rw[0], off);
+      v.w[1][j] = buffer_load16(rw[1], off);
+      v.x[j] = buffer_load16(rx, off);
+    }
+  };
+  f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  auto use = [&](const Unit& v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        acc[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v.w[k][j]),
+                                                         __builtin_bit_cast(bf16x8, v.x[j]), acc[k], 0, 0, 0);
+    mfma_done(acc[0]);
+    mfma_done(acc[1]);
+  };
+  const int units = (kbytes + kUnitBytes - 1) / kUnitBytes;
+  constexpr int kStep = kSplit ? kFewWaves : 1;
+  Unit va, vb;
+  int u = kSplit ? wave : 0;
+  if (u < units) load(va, u);
+  while (u < units) {
+    if (u + kStep < units) load(vb, u + kStep);
+    use(va);
+    u += kStep;
+    if (u >= units) break;
+    if (u + kStep < units) load(va, u + kStep);
+    use(vb);
+    u += kStep;
+  }
+  if constexpr (kSplit) {
+    part[wave][0][lane] = acc[0];
+    part[wave][1][lane] = acc[1];
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const f32x4 q = part[v][k][lane];
+        acc[k].x += q.x; acc[k].y += q.y; acc[k].z += q.z; acc[k].w += q.w;
+      }
+  }
+  // the lane holds columns 4 (lane / 16) .. +3 of row lane % 16
+  if (l16 < nrows && 4 * grp < ncols) {
+    const int64_t p = row0 + l16;
+    const int c = c0 + 4 * grp;
+    const f32x4 a = acc[0], b = acc[1];
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + p * I + c) =
+        make_uint2(pack_bf16x2(glu(a.x, b.x), glu(a.y, b.y)), pack_bf16x2(glu(a.z, b.z), glu(a.w, b.w)));
+    if (gu) {
+      *reinterpret_cast<uint2*>(gu + p * 2 * I + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+      *reinterpret_cast<uint2*>(gu + p * 2 * I + I + c) = make_uint2(pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+    }
+  }
+}
+
+hipError_t launch_glu_few_rows(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
+  const int64_t tiles = (g.nout + 15) / 16, slots = (int64_t)g.M / 16 + std::min(g.E, g.M);
+  const int64_t units = (2 * (int64_t)g.kc + kUnitBytes - 1) / kUnitBytes;
+  if (units >= 2 * kFewWaves || slots * tiles < 4096)
+    glu_few_rows_kernel<true><<<(unsigned)items_grid(slots * tiles), 64 * kFewWaves, 0, s>>>(g, gu);
+  else
+    glu_few_rows_kernel<false>
+        <<<(unsigned)items_grid(slots * ((tiles + kFewWaves - 1) / kFewWaves)), 64 * kFewWaves, 0, s>>>(g, gu);
+  return hipGetLastError();
+}
+
+// Whether the weights stream past the rows.  us of the whole block here and in
+// tiles, the same number of rows for each expert, weights from HBM:
+//   rows an expert                       1         8        16        24
+//     E = 64, H = 2048, I = 1024   151, 179  166, 191  156, 177  223, 179
+//     E = 8, H = I = 4096          157, 177  161, 184  169, 190  226, 191
+//     E = 32, H = I = 2880         263, 267  283, 283  299, 283  426, 284
+//     E = 128, H = 2048, I = 768   208, 234  226, 251  230, 246  325, 249
+// so up to 16 rows, which are one pass over the weights; at 8 on average hardly
+// an expert has more.
+// A grid holds less than 2^32 threads; beyond that the tiles serve.
+bool streams(const GroupedArgs& g) {
+  const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
+  return g.M <= 8 * (int64_t)g.E && items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
+}
+
+// Whether tiles of 128 columns of h (256 of dh) leave compute units without work:
+// those of half the columns then do better.  Eight rows in all, the gate_up
+// product in small and in large tiles: E = 64, H = 2048, I = 1024 32 and 37 us,
+// H = I = 2880 47 and 57 us (whole block).
+bool few_tiles(const GroupedArgs& g) {
+  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
+  return rows * ((g.nout + 127) / 128) <= 128;
+}
+
 template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
 hipError_t launch_glu_tiles(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
   using Big = GluTile<kNWN, kNWM, kTM, kBufsA, kBufsB>;
@@ -218,10 +339,14 @@ hipError_t launch_backward_tiles(const GroupedArgs& g, const uint16_t* gu, uint1
 }  // namespace
 
 hipError_t launch_glu(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
+  if (streams(g)) return launch_glu_few_rows(g, gu, s);
+  if (few_tiles(g)) return launch_glu_tiles<2, 4, 2, 3, 3>(g, gu, s);
   return launch_glu_tiles<4, 2, 4, 3, 2>(g, gu, s);
 }
 
 hipError_t launch_glu_backward(const GroupedArgs& g, const uint16_t* gu, uint16_t* dgu, hipStream_t s) {
+  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
+  if (rows * ((g.nout + 255) / 256) <= 128) return launch_backward_tiles<4, 2, 1, 4, 3, 3>(g, gu, dgu, s);
   return launch_backward_tiles<4, 2, 2, 4, 3, 2>(g, gu, dgu, s);
 }
 

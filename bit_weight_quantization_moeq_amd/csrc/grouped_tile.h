@@ -571,7 +571,8 @@ __device__ __forceinline__ int work_item(int total, int run) {
 int64_t items_grid(int64_t total) { return (total + total / 4 + 2 * kXcds - 1) / kXcds * kXcds; }
 
 // The (expert, row tile, column tile) triples, expert-major.  An expert's rows
-// are cut into ceil(rows / max_rows) near-equal tiles, taken in groups of
+// are cut into ceil(rows / max_rows) tiles, whole ones and a rest where equal
+// ones would be nearly whole, otherwise equal ones, taken in groups of
 // kTileGroup that go through the column tiles together.  Each wave scans the
 // experts by itself, 64 at a time.
 __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int max_rows, int ncol, int& e, int& row0, int& nrows,
@@ -602,7 +603,11 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& g, int max_rows, in
     ct = rr / gt;
     const int mt = grp * kTileGroup + (rr - ct * gt);
     if (mt >= k) return true;   // (only offsets that do not ascend come here)
-    const int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
+    int a = (int)((int64_t)mt * c / k), b = (int)((int64_t)(mt + 1) * c / k);
+    if (4 * ((c + k - 1) / k) > 3 * max_rows) {   // equal tiles would cost as much as whole ones
+      a = mt * max_rows;
+      b = min(a + max_rows, c);
+    }
     row0 = r0 + a;
     nrows = b - a;
     return true;
