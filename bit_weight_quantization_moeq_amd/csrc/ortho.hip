@@ -84,8 +84,9 @@ __global__ __launch_bounds__(256) void ortho_squares_kernel(const T* g, int64_t 
 template <typename T>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N, int32_t K, int32_t xc, bool wide,
                                                           const double* partial, int32_t chunks, double times, _Float16* x) {
-  double sum = 0.0;
-  for (int i = 0; i < chunks; ++i) sum += partial[(int64_t)blockIdx.y * chunks + i];
+  static_assert(kMaxChunks == 64, "a partial sum a lane");
+  const int lane = threadIdx.x & 63;
+  const double sum = wave_sum(lane < chunks ? partial[(int64_t)blockIdx.y * chunks + lane] : 0.0);
   const double f = sum == 0.0 ? 0.0 : times / sqrt(sum);   // (an infinity or a NaN of G: NaN or 0 times inf below)
   // in fp32 where it can hold the factor (the same to fp16's rounding), which is quicker
   const bool narrow = f > 0x1p-100 && f < 0x1p100;
@@ -544,8 +545,9 @@ hipError_t launch_start(const T* g, const OrthoPlan& p, double times, double* pa
   ortho_squares_kernel<T><<<dim3(p.chunks, p.E), 256, 0, s>>>(g, size, aligned && size % 8 == 0, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t blocks = ((int64_t)p.N * (p.xc / 8) + 255) / 256;
-  ortho_scale_kernel<T><<<dim3((unsigned)std::min<int64_t>(blocks, 1 << 16), p.E), 256, 0, s>>>(
+  // (a workgroup takes several turns: each begins with the norm)
+  const int64_t blocks = ((int64_t)p.N * (p.xc / 8) + 255) / 256, most = std::max<int64_t>(1, 8192 / p.E);
+  ortho_scale_kernel<T><<<dim3((unsigned)std::min(blocks, most), p.E), 256, 0, s>>>(
       g, p.N, p.K, p.xc, aligned && p.K % 8 == 0, partial, p.chunks, times, x);
   return hipGetLastError();
 }
