@@ -24,8 +24,6 @@ namespace moeq {
 namespace {
 
 constexpr int kShift = 8;   // A and P are stored times 2^kShift
-constexpr int kChunk = 1 << 15;   // values per partial sum, at least
-constexpr int kMaxChunks = 64;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 __device__ __forceinline__ float value(const uint16_t* p) { return bf16_value(*p); }
@@ -84,7 +82,7 @@ __global__ __launch_bounds__(256) void ortho_squares_kernel(const T* g, int64_t 
 template <typename T>
 __global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N, int32_t K, int32_t xc, bool wide,
                                                           const double* partial, int32_t chunks, double times, _Float16* x) {
-  static_assert(kMaxChunks == 64, "a partial sum a lane");
+  static_assert(kOrthoMaxChunks == 64, "a partial sum a lane");
   const int lane = threadIdx.x & 63;
   const double sum = wave_sum(lane < chunks ? partial[(int64_t)blockIdx.y * chunks + lane] : 0.0);
   const double f = sum == 0.0 ? 0.0 : times / sqrt(sum);   // (an infinity or a NaN of G: NaN or 0 times inf below)
@@ -365,9 +363,11 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
           v[2] = __builtin_bit_cast(float, q.y << 16);
           v[3] = __builtin_bit_cast(float, q.y & 0xffff0000u);
         } else {
-          const u32x4 q = buffer_load16(from, (uint32_t)off);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(float, q[j]);
+          const float4 q = __builtin_bit_cast(float4, buffer_load16(from, (uint32_t)off));
+          v[0] = q.x;
+          v[1] = q.y;
+          v[2] = q.z;
+          v[3] = q.w;
         }
       } else
 #pragma unroll
@@ -535,9 +535,6 @@ hipError_t launch_few(const T* g, const OrthoPlan& p, const OrthoSteps& table, i
   return hipGetLastError();
 }
 
-int32_t pad8(int32_t n) { return (n + 7) / 8 * 8; }
-int64_t round256(int64_t n) { return (n + 255) / 256 * 256; }
-
 template <typename T>
 hipError_t launch_start(const T* g, const OrthoPlan& p, double times, double* partial, _Float16* x, hipStream_t s) {
   const int64_t size = (int64_t)p.N * p.K;
@@ -553,27 +550,6 @@ hipError_t launch_start(const T* g, const OrthoPlan& p, double times, double* pa
 }
 
 }  // namespace
-
-OrthoPlan ortho_plan(int32_t E, int32_t N, int32_t K) {
-  OrthoPlan p;
-  p.E = E;
-  p.N = N;
-  p.K = K;
-  p.tall = N > K;
-  p.n = std::min(N, K);
-  p.m = std::max(N, K);
-  p.xc = pad8(K);
-  p.nc = pad8(p.n);
-  p.chunks = (int32_t)std::min<int64_t>(kMaxChunks, ((int64_t)N * K + kChunk - 1) / kChunk);
-  const int64_t x = round256((int64_t)E * N * p.xc * 2), a = round256((int64_t)E * p.n * p.nc * 2);
-  p.partial = 0;
-  p.x = round256((int64_t)E * p.chunks * 8);
-  p.y = p.x + x;
-  p.a = p.y + x;
-  p.p = p.a + a;
-  p.bytes = p.p + a;
-  return p;
-}
 
 hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p, const float* coefficients, int32_t steps,
                                 uint16_t* out, void* workspace, hipStream_t s) {

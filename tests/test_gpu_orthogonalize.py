@@ -8,11 +8,22 @@ entries and ||.|| its largest singular value, one step adds
   dA = 2^-11 |A| + L 2^-23 | |X||X^T| |
   dP = (|b| + 2 |c| ||A||) dA + 2^-11 |P| + (n + 4) 2^-23 (|a| sqrt(n) + |b| |A| + |c| | |A||A| |)
   dX = dP ||X|| + 2^-11 |X'| + n 2^-23 | |P||X| |
-to its result, and an error of its input reaches the result times at most
-max |f'(s)| over the singular values s, f(s) = a s + b s^3 + c s^5 (the step maps
-singular values by f, and differences of two of them by f's difference
-quotients).  The output's rounding to bf16 is 2^-8 of it.  Second-order terms are
-below a tenth of this: 1.1."""
+to its result.  An error E of its input reaches the result through the step's
+derivative, which in the exact iterate's singular basis multiplies the entries of
+E's symmetric part by (f(s) - f(t)) / (s - t), those of its antisymmetric part by
+(f(s) + f(t)) / (s + t), and what lies outside the shorter side's space by f(s) / s,
+with s, t the singular values and f(s) = a s + b s^3 + c s^5: at most the largest of
+these.  The output's rounding to bf16 is 2^-8 of it.  Second-order terms are below
+a tenth of this: 1.1.
+
+That is the worst case, 6 to 40 % of the result.  Matrices of 64 entries and more
+are held to what to expect, too: roundings are independent and spread evenly over
+the half steps (the 2-norm over the square root of 3), an error matrix has no
+direction of its own, so that squares add, a step multiplies by the factors' root
+mean square over all entries, and |E X| is |E| |X| / sqrt(n) for a random n x n E.
+Three times that (sums over 64 entries and more stray far less).  It grows with
+missing directions, whose rounding a step multiplies by a as it does small singular
+values: a matrix of rank one is 10 % off after five steps, one of full rank 0.2 %."""
 
 import numpy as np
 import pytest
@@ -38,43 +49,57 @@ def _norm(m):
     return float(np.sqrt((np.asarray(m) ** 2).sum()))
 
 
-def _steepest(top, abc):
+def _factors(s, abc, m):
+    """Of the factors by which a step multiplies the parts of its input's error:
+    the largest, and the root mean square over n x m entries."""
     a, b, c = abc
-    at = [0.0, top]
-    if b * c < 0 and 0 < -0.3 * b / c < top * top:
-        at.append(np.sqrt(-0.3 * b / c))
-    return max(abs(a + 3 * b * s ** 2 + 5 * c * s ** 4) for s in at)
+    s, t = s[:, None], s[None, :]
+    # (f(s) -+ f(t)) / (s -+ t) without the quotient
+    minus = a + b * (s * s + s * t + t * t) + c * (s ** 4 + s ** 3 * t + s * s * t * t + s * t ** 3 + t ** 4)
+    plus = a + b * (s * s - s * t + t * t) + c * (s ** 4 - s ** 3 * t + s * s * t * t - s * t ** 3 + t ** 4)
+    out = a + b * s * s + c * s ** 4
+    n = minus.shape[0]
+    mean = (((minus ** 2 + plus ** 2) / 2).sum() + (m - n) * (out ** 2).sum()) / (n * m)
+    return max(np.abs(minus).max(), np.abs(plus).max(), np.abs(out).max()), np.sqrt(mean)
 
 
 def _bound(g, table):
-    """What the result's 2-norm may be off by, and the exact result."""
+    """What the result may be off by at most, what to expect, and the exact result."""
     x = start(g)
     if x.shape[0] > x.shape[1]:
         x = x.T
     n, m = x.shape
     tiny = 2.0 ** -25 * 2.0 ** -min(15, int(np.log2(m) / 2))
     err = H * _norm(x) + tiny * np.sqrt(n * m)
+    rms, even = err / np.sqrt(3), H / np.sqrt(3)
     for a, b, c in table:
         A = x @ x.T
         A2, P = A @ A, a * np.eye(n) + b * A
         P = P + c * A2
         y = step(x, (a, b, c))
-        top, topA = np.linalg.norm(x, 2), np.linalg.norm(A, 2)
+        values = np.linalg.svd(x, compute_uv=False)
+        top, topA = values[0], values[0] ** 2
         dA = H * _norm(A) + m * S * _norm(np.abs(x) @ np.abs(x.T)) + 2.0 ** -33 * n
         dP = (abs(b) + 2 * abs(c) * topA) * dA + H * _norm(P) + 2.0 ** -33 * n
         dP += (n + 4) * S * (abs(a) * np.sqrt(n) + abs(b) * _norm(A) + abs(c) * _norm(np.abs(A) @ np.abs(A)))
         dX = dP * top + H * _norm(y) + n * S * _norm(np.abs(P) @ np.abs(x)) + tiny * np.sqrt(n * m)
-        err = err * _steepest(top + err, (a, b, c)) + dX
+        most, mean = _factors(values, (a, b, c), m)
+        err = err * most + dX
+        lam = values ** 2
+        poly = np.sqrt(np.mean((b + c * (lam[:, None] + lam[None, :])) ** 2)) * even * _norm(A)
+        rms = np.sqrt((rms * mean) ** 2 + (poly ** 2 + (even * _norm(P)) ** 2) * _norm(x) ** 2 / n + (even * _norm(y)) ** 2)
         x = y
-    return 1.1 * err + 2.0 ** -8 * _norm(x), x if np.shape(g)[0] <= np.shape(g)[1] else x.T
+    expected = np.sqrt(rms ** 2 + (2.0 ** -8 * _norm(x)) ** 2 / 3)
+    return 1.1 * err + 2.0 ** -8 * _norm(x), expected, x if np.shape(g)[0] <= np.shape(g)[1] else x.T
 
 
 def _check(g, out, table=(COEFFICIENTS,) * 5):
     g, out = _f64(g), _f64(out)
     for e in range(g.shape[0]):
-        tol, want = _bound(g[e], table)
+        tol, expected, want = _bound(g[e], table)
         off = _norm(out[e] - want)
         assert off <= tol, (e, off, tol)
+        assert want.size < 64 or off <= 3 * expected, (e, off, expected, _norm(want))
 
 
 SHAPES = [(1, 1, 1), (2, 1, 300), (2, 300, 1), (3, 3, 3), (3, 16, 72), (2, 72, 16), (2, 40, 41), (2, 41, 40), (2, 64, 64),
@@ -197,7 +222,7 @@ def test_other_stream_and_graph():
 def test_oracle_side():
     """(the bound's exact result is the oracle's)"""
     g = np.random.default_rng(10).standard_normal((12, 7))
-    assert np.allclose(_bound(g, (COEFFICIENTS,) * 5)[1], orthogonalize(g), atol=1e-12)
+    assert np.allclose(_bound(g, (COEFFICIENTS,) * 5)[2], orthogonalize(g), atol=1e-12)
 
 
 # (rows up to 16 and up to 32, either side long, columns up to 2048 and beyond, and what is past them)
@@ -213,3 +238,29 @@ def test_few_rows(shape, dtype):
     pick = [0, shape[0] - 1]
     _check(g[pick], out.t[pick])
     assert torch.equal(out.t, moeq.moeq_orthogonalize(g))
+
+
+@pytest.mark.parametrize("shape", [(3, 64, 16), (3, 16, 64), (2, 72, 12), (2, 2048, 16), (1, 4096, 32), (2, 9, 200), (2, 130, 300),
+                                   (2, 300, 130)])
+@pytest.mark.parametrize("rank", [1, 3, 1000])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ranks(shape, rank, dtype):
+    """Gradients of experts with few rows have few directions."""
+    say(f"orthogonalize {shape} rank {rank} {dtype}")
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    E, N, K = shape
+    r = min(rank, N, K)
+    u, v = (torch.randn(s, generator=gen, device=DEV) for s in ((E, N, r), (E, r, K)))
+    g = (torch.randn(shape, generator=gen, device=DEV) if rank == 1000 else u @ v).to(dtype)
+    _check(g, moeq.moeq_orthogonalize(g))
+
+
+def test_one_entry_at_a_time():
+    """With (a, b, c) = (1, 0, 0) the update is G / |G|: every entry keeps its place."""
+    say("orthogonalize places")
+    for N, K in ((20, 4), (4, 20), (64, 16), (32, 40), (40, 32), (70, 90)):
+        for dtype in (BF16, F32):
+            g = torch.zeros((N * K, N, K), dtype=dtype, device=DEV)
+            g.view(N * K, N * K).fill_diagonal_(3.0)
+            g = g[::7].contiguous()
+            assert torch.equal(moeq.moeq_orthogonalize(g, 1, (1.0, 0.0, 0.0)), (g / 3).to(BF16)), (N, K, dtype)
