@@ -1077,18 +1077,18 @@ def moeq_grouped_ffn(x, gate_up, down, offsets, save=False, out=None, gu=None, w
     for the rows ``offsets[e] <= p < offsets[e+1]`` of each expert e.  ``x``
     ``[M, H]``, ``gate_up`` ``[E, 2I, H]`` (gate rows first), ``down``
     ``[E, H, I]``, ``offsets`` int32 ``[E+1]`` on the device; returns ``out``
-    bf16 ``[M, H]``, with ``save`` (or a buffer ``gu``) also ``gu`` bf16
+    bf16 ``[M, H]``, with ``save`` (or a buffer ``gu``) also ``gu`` fp32
     ``[M, 2I]`` for :func:`moeq_grouped_ffn_backward`.  Rows outside
     ``[offsets[0], offsets[E])`` are not written.  H and I are multiples of 8."""
     M, E, H, I = _grouped_ffn(x, gate_up, down, offsets)
     if out is not None:
         _dev(out, torch.bfloat16, "out", (M, H))
     if gu is not None:
-        _dev(gu, torch.bfloat16, "gu", (M, 2 * I))
+        _dev(gu, torch.float32, "gu", (M, 2 * I))
     dev = _on_device("moeq_grouped_ffn", x, gate_up, down, offsets, out, gu)
     y = _empty((M, H), torch.bfloat16, dev, stream) if out is None else out
     if save and gu is None:
-        gu = _empty((M, 2 * I), torch.bfloat16, dev, stream)
+        gu = _empty((M, 2 * I), torch.float32, dev, stream)
     lib = _load()
     workspace = _workspace_for(workspace, int(lib.moeq_grouped_ffn_workspace_bytes(M, E, H, I)), dev, stream)
     with _current(dev):
@@ -1113,7 +1113,7 @@ def moeq_grouped_ffn_backward(grad_out, x, gate_up, down, offsets, gu, dtype=tor
     written."""
     M, E, H, I = _grouped_ffn(x, gate_up, down, offsets)
     _dev(grad_out, torch.bfloat16, "grad_out", (M, H))
-    _dev(gu, torch.bfloat16, "gu", (M, 2 * I))
+    _dev(gu, torch.float32, "gu", (M, 2 * I))
     if grad_x is not None:
         _dev(grad_x, torch.bfloat16, "grad_x", (M, H))
     given = next((t for t in (grad_gate_up, grad_down) if t is not None), None)

@@ -40,7 +40,7 @@ size_t moeq_grouped_ffn_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t
 }
 
 moeq_status moeq_grouped_ffn(const uint16_t* x, const uint16_t* gate_up, const uint16_t* down, const int32_t* offsets,
-                             int32_t M, int32_t E, int32_t H, int32_t I, uint16_t* gu_saved, uint16_t* out,
+                             int32_t M, int32_t E, int32_t H, int32_t I, float* gu_saved, uint16_t* out,
                              void* workspace, size_t workspace_bytes, void* stream) {
   moeq_status st = check_ffn(M, E, H, I);
   if (st != MOEQ_OK) return st;
@@ -52,7 +52,7 @@ moeq_status moeq_grouped_ffn(const uint16_t* x, const uint16_t* gate_up, const u
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != MOEQ_OK) return st;
   const Span in = bf16(x, M, H), w1 = bf16(gate_up, (int64_t)E * 2 * I, H), w2 = bf16(down, (int64_t)E * H, I),
-             off = ints(offsets, E), gu = {gu_saved, gu_saved ? (int64_t)M * 2 * I * 2 : 0}, y = bf16(out, M, H),
+             off = ints(offsets, E), gu = {gu_saved, gu_saved ? (int64_t)M * 2 * I * 4 : 0}, y = bf16(out, M, H),
              ws = {workspace, (int64_t)need};
   if (overlaps(ws, {in, w1, w2, off}) || overlaps(gu, {in, w1, w2, off, ws}) || overlaps(y, {in, w1, w2, off, ws, gu}))
     return MOEQ_EINVAL;
@@ -68,7 +68,7 @@ size_t moeq_grouped_ffn_backward_workspace_bytes(int32_t M, int32_t E, int32_t H
 }
 
 moeq_status moeq_grouped_ffn_backward(const uint16_t* grad_out, const uint16_t* x, const uint16_t* gate_up,
-                                      const uint16_t* down, const int32_t* offsets, const uint16_t* gu_saved, int32_t M,
+                                      const uint16_t* down, const int32_t* offsets, const float* gu_saved, int32_t M,
                                       int32_t E, int32_t H, int32_t I, int32_t dtype, uint16_t* grad_x,
                                       void* grad_gate_up, void* grad_down, void* workspace, size_t workspace_bytes,
                                       void* stream) {
@@ -79,14 +79,14 @@ moeq_status moeq_grouped_ffn_backward(const uint16_t* grad_out, const uint16_t* 
   if (M > 0 && (!grad_out || !x || !gate_up || !down || !gu_saved || !grad_x)) return MOEQ_EINVAL;
   if (!aligned16(grad_gate_up) || !aligned16(grad_down)) return MOEQ_EALIGN;
   if (M > 0)
-    for (const uint16_t* p : {grad_out, x, gate_up, down, gu_saved, static_cast<const uint16_t*>(grad_x)})
-      if (!aligned16(p)) return MOEQ_EALIGN;
+    for (const uint16_t* p : {grad_out, x, gate_up, down, static_cast<const uint16_t*>(grad_x)})
+      if (!aligned16(p) || !aligned16(gu_saved)) return MOEQ_EALIGN;
   const size_t need = moeq_grouped_ffn_backward_workspace_bytes(M, E, H, I);
   st = check_workspace(workspace, workspace_bytes, need);
   if (st != MOEQ_OK) return st;
   const int64_t size = dtype == MOEQ_DTYPE_FP32 ? 4 : 2, w1n = (int64_t)E * 2 * I * H, w2n = (int64_t)E * H * I;
   const Span dy = bf16(grad_out, M, H), in = bf16(x, M, H), w1 = {gate_up, M ? w1n * 2 : 0}, w2 = {down, M ? w2n * 2 : 0},
-             off = ints(offsets, E), gu = bf16(gu_saved, M, 2 * I), dx = bf16(grad_x, M, H),
+             off = ints(offsets, E), gu = {gu_saved, (int64_t)M * 2 * I * 4}, dx = bf16(grad_x, M, H),
              dw1 = {grad_gate_up, w1n * size}, dw2 = {grad_down, w2n * size}, ws = {workspace, (int64_t)need};
   if (overlaps(ws, {dy, in, w1, w2, off, gu}) || overlaps(dx, {dy, in, w1, w2, off, gu, ws}) ||
       overlaps(dw1, {dy, in, w1, w2, off, gu, ws, dx}) || overlaps(dw2, {dy, in, w1, w2, off, gu, ws, dx, dw1}))

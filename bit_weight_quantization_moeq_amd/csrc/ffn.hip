@@ -7,16 +7,16 @@
 //   dg     = dh u s (1 + g (1 - s))     du = dh g s
 //
 // Two kernels here carry the activation in the epilogue of a product: the
-// gate_up product stores h (and, for training, g and u in bf16), the down
+// gate_up product stores h (and, for training, g and u in fp32), the down
 // product's input gradient stores dg | du and h again.  The other products of
 // the block are those of grouped.hip on what these store.  A tile of the
 // gate_up product holds the same columns of the gate and of the up projection,
 // 32 of each in turn, so that a wave has g and u of a value in the same lane.
 //
-// Roundings: g, u and dh are fp32 sums.  h, dg and du are rounded to bf16
-// because the next product's matrix instructions take bf16; g and u are kept
-// in bf16 for the backward pass, which doubles the rounding of h, dg and du
-// (2^-9 relative each) and halves what training has to hold and move.
+// Roundings: g, u and dh are fp32 sums, and g and u are kept so for the backward
+// pass (in bf16, half the bytes, their rounding would be as large again as the
+// gradients' own: 3.5e-3 of grad_down instead of 2.4e-3).  h, dg and du are
+// rounded to bf16, because the next product's matrix instructions take bf16.
 #include "grouped_tile.h"
 
 #include "ffn.h"
@@ -34,10 +34,11 @@ template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
 struct GluTile {
   using T = Tile<Op::kBf16, false, false, kNWN, kNWM, 2, kTM, kBufsA, kBufsB, true>;
   static constexpr int kCols = T::kCols / 2;
-  static constexpr int kPitch = 64 + 16, kPiece = 3 * 32 * kPitch;   // 32 rows of 32 columns of h, g and u
+  // 32 rows of 32 columns of h in bf16, and of g and u in fp32
+  static constexpr int kPitch = 64 + 16, kWide = 128 + 16, kPiece = 32 * (kPitch + 2 * kWide);
   static constexpr int kLds = imax(T::kLds, T::kNW * kPiece);
 
-  __device__ __forceinline__ static void run(char* smem, const GroupedArgs& g, uint16_t* gu, int e, int row0, int nrows,
+  __device__ __forceinline__ static void run(char* smem, const GroupedArgs& g, float* gu, int e, int row0, int nrows,
                                              int c0) {
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int kbytes = 2 * g.kc, I = g.nout;
@@ -57,13 +58,8 @@ struct GluTile {
     const int wn = wave % kNWN, wm = wave / kNWN, l32 = lane & 31, h = lane >> 5;
     char* buf = smem + wave * kPiece;
     const int c = c0 + 32 * wn + 8 * (lane & 3);
-    auto put = [&](int plane, int q, const float (&v)[4]) {
-      *reinterpret_cast<uint2*>(buf + (32 * plane + l32) * kPitch + 2 * (8 * q + 4 * h)) =
-          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    };
-    auto get = [&](int plane, int r) {
-      return *reinterpret_cast<const u32x4*>(buf + (32 * plane + r) * kPitch + 16 * (lane & 3));
-    };
+    char* wide = buf + 32 * kPitch;
+    const int cw = c0 + 32 * wn + 4 * (lane & 7);
 #pragma unroll
     for (int m = 0; m < kTM; ++m) {
       const int r0 = 32 * (kTM * wm + m);
@@ -77,10 +73,12 @@ struct GluTile {
           uv[i] = acc[1][m][4 * q + i];
           hv[i] = glu(gv[i], uv[i]);
         }
-        put(0, q, hv);
+        *reinterpret_cast<uint2*>(buf + l32 * kPitch + 2 * (8 * q + 4 * h)) =
+            make_uint2(pack_bf16x2(hv[0], hv[1]), pack_bf16x2(hv[2], hv[3]));
         if (gu) {
-          put(1, q, gv);
-          put(2, q, uv);
+          char* p = wide + l32 * kWide + 4 * (8 * q + 4 * h);
+          *reinterpret_cast<float4*>(p) = make_float4(gv[0], gv[1], gv[2], gv[3]);
+          *reinterpret_cast<float4*>(p + 32 * kWide) = make_float4(uv[0], uv[1], uv[2], uv[3]);
         }
       }
       // (a wave's LDS accesses are done in order)
@@ -89,15 +87,22 @@ struct GluTile {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = 16 * k + lane / 4;
-        if (r0 + r < nrows && c < I) {
-          const int64_t p = row0 + r0 + r;
-          __builtin_nontemporal_store(get(0, r), reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + p * I + c));
-          if (gu) {
-            __builtin_nontemporal_store(get(1, r), reinterpret_cast<u32x4*>(gu + p * 2 * I + c));
-            __builtin_nontemporal_store(get(2, r), reinterpret_cast<u32x4*>(gu + p * 2 * I + I + c));
+        if (r0 + r < nrows && c < I)
+          __builtin_nontemporal_store(
+              *reinterpret_cast<const u32x4*>(buf + r * kPitch + 16 * (lane & 3)),
+              reinterpret_cast<u32x4*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + r0 + r) * I + c));
+      }
+      if (gu)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 8 * k + lane / 8;
+          if (r0 + r < nrows && cw < I) {
+            float* to = gu + (int64_t)(row0 + r0 + r) * 2 * I + cw;
+            const char* from = wide + r * kWide + 16 * (lane & 7);
+            __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(from), reinterpret_cast<u32x4*>(to));
+            __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(from + 32 * kWide), reinterpret_cast<u32x4*>(to + I));
           }
         }
-      }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
     }
@@ -105,7 +110,7 @@ struct GluTile {
 };
 
 template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
-__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_kernel(GroupedArgs g, uint16_t* gu) {
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_kernel(GroupedArgs g, float* gu) {
   using Big = GluTile<kNWN, kNWM, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[Big::kLds];
   int e, row0, nrows, ct;
@@ -123,7 +128,7 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_kernel(
 
 // dh of a tile, and from it and g | u: dg | du and h.
 template <int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
-__device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs& g, const uint16_t* gu, uint16_t* dgu, int e,
+__device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs& g, const float* gu, uint16_t* dgu, int e,
                                                   int row0, int nrows, int c0) {
   using T = Tile<Op::kBf16, true, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -141,7 +146,7 @@ __device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs&
   T::run(smem, a, b, nullptr, 0, (kbytes + kStepBytes - 1) / kStepBytes, acc);
 
   struct Pair {
-    u32x4 g, u;
+    float4 g[2], u[2];
   };
   gu += (int64_t)row0 * 2 * I + c0;
   dgu += (int64_t)row0 * 2 * I + c0;
@@ -149,18 +154,20 @@ __device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs&
   T::each8(
       smem, acc, nrows, min(T::kCols, I - c0),
       [&](int r, int c) {
-        const uint16_t* p = gu + (int64_t)r * 2 * I + c;
-        return Pair{*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + I)};
+        const float4* p = reinterpret_cast<const float4*>(gu + (int64_t)r * 2 * I + c);
+        const float4* q = reinterpret_cast<const float4*>(gu + (int64_t)r * 2 * I + I + c);
+        return Pair{{p[0], p[1]}, {q[0], q[1]}};
       },
       [&](int r, int c, const float (&dh)[8], const Pair& in) {
         u32x4 dgv, duv, hv;
+        const float gs[8] = {in.g[0].x, in.g[0].y, in.g[0].z, in.g[0].w, in.g[1].x, in.g[1].y, in.g[1].z, in.g[1].w};
+        const float us[8] = {in.u[0].x, in.u[0].y, in.u[0].z, in.u[0].w, in.u[1].x, in.u[1].y, in.u[1].z, in.u[1].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float o[3][2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float gv = __builtin_bit_cast(float, j ? in.g[i] & 0xffff0000u : in.g[i] << 16);
-            const float uv = __builtin_bit_cast(float, j ? in.u[i] & 0xffff0000u : in.u[i] << 16);
+            const float gv = gs[2 * i + j], uv = us[2 * i + j];
             const float s = sigmoid(gv), d = dh[2 * i + j];
             o[0][j] = d * uv * (s * (1.0f + gv * (1.0f - s)));
             o[1][j] = d * (gv * s);
@@ -178,7 +185,7 @@ __device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs&
 }
 
 template <int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
-__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_backward_kernel(GroupedArgs g, const uint16_t* gu,
+__global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_backward_kernel(GroupedArgs g, const float* gu,
                                                                                        uint16_t* dgu) {
   using Big = Tile<Op::kBf16, true, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   __shared__ __attribute__((aligned(16))) char smem[imax(Big::kLds, Big::out_bytes(4))];
@@ -204,7 +211,7 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void glu_backwar
 constexpr int kUnitBytes = 256, kFewWaves = 4;
 
 template <bool kSplit>
-__global__ __launch_bounds__(64 * kFewWaves) void glu_few_rows_kernel(GroupedArgs g, uint16_t* gu) {
+__global__ __launch_bounds__(64 * kFewWaves) void glu_few_rows_kernel(GroupedArgs g, float* gu) {
   constexpr int kCols = kSplit ? 16 : 16 * kFewWaves;   // of a workgroup
   __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][2][64];
   int e, row0, nrows, ct;
@@ -277,13 +284,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void glu_few_rows_kernel(GroupedArg
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + p * I + c) =
         make_uint2(pack_bf16x2(glu(a.x, b.x), glu(a.y, b.y)), pack_bf16x2(glu(a.z, b.z), glu(a.w, b.w)));
     if (gu) {
-      *reinterpret_cast<uint2*>(gu + p * 2 * I + c) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
-      *reinterpret_cast<uint2*>(gu + p * 2 * I + I + c) = make_uint2(pack_bf16x2(b.x, b.y), pack_bf16x2(b.z, b.w));
+      *reinterpret_cast<f32x4*>(gu + p * 2 * I + c) = a;
+      *reinterpret_cast<f32x4*>(gu + p * 2 * I + I + c) = b;
     }
   }
 }
 
-hipError_t launch_glu_few_rows(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
+hipError_t launch_glu_few_rows(const GroupedArgs& g, float* gu, hipStream_t s) {
   const int64_t tiles = (g.nout + 15) / 16, slots = (int64_t)g.M / 16 + std::min(g.E, g.M);
   const int64_t units = (2 * (int64_t)g.kc + kUnitBytes - 1) / kUnitBytes;
   if (units >= 2 * kFewWaves || slots * tiles < 4096)
@@ -319,7 +326,7 @@ bool few_tiles(const GroupedArgs& g) {
 }
 
 template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
-hipError_t launch_glu_tiles(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
+hipError_t launch_glu_tiles(const GroupedArgs& g, float* gu, hipStream_t s) {
   using Big = GluTile<kNWN, kNWM, kTM, kBufsA, kBufsB>;
   const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
   const int64_t grid = items_grid(((int64_t)g.M / Big::T::kRows + std::min(g.E, g.M)) * ncol);
@@ -328,7 +335,7 @@ hipError_t launch_glu_tiles(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
 }
 
 template <int kNWN, int kNWM, int kTN, int kTM, int kBufsA, int kBufsB>
-hipError_t launch_backward_tiles(const GroupedArgs& g, const uint16_t* gu, uint16_t* dgu, hipStream_t s) {
+hipError_t launch_backward_tiles(const GroupedArgs& g, const float* gu, uint16_t* dgu, hipStream_t s) {
   using Big = Tile<Op::kBf16, true, false, kNWN, kNWM, kTN, kTM, kBufsA, kBufsB>;
   const int64_t ncol = (g.nout + Big::kCols - 1) / Big::kCols;
   const int64_t grid = items_grid(((int64_t)g.M / Big::kRows + std::min(g.E, g.M)) * ncol);
@@ -338,13 +345,13 @@ hipError_t launch_backward_tiles(const GroupedArgs& g, const uint16_t* gu, uint1
 
 }  // namespace
 
-hipError_t launch_glu(const GroupedArgs& g, uint16_t* gu, hipStream_t s) {
+hipError_t launch_glu(const GroupedArgs& g, float* gu, hipStream_t s) {
   if (streams(g)) return launch_glu_few_rows(g, gu, s);
   if (few_tiles(g)) return launch_glu_tiles<2, 4, 2, 3, 3>(g, gu, s);
   return launch_glu_tiles<4, 2, 4, 3, 2>(g, gu, s);
 }
 
-hipError_t launch_glu_backward(const GroupedArgs& g, const uint16_t* gu, uint16_t* dgu, hipStream_t s) {
+hipError_t launch_glu_backward(const GroupedArgs& g, const float* gu, uint16_t* dgu, hipStream_t s) {
   const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
   if (rows * ((g.nout + 255) / 256) <= 128) return launch_backward_tiles<4, 2, 1, 4, 3, 3>(g, gu, dgu, s);
   return launch_backward_tiles<4, 2, 2, 4, 3, 2>(g, gu, dgu, s);

@@ -548,11 +548,10 @@ moeq_status moeq_grouped_mm_fp8(const moeq_qweight *x, const moeq_qweight *w, co
  *   gate_up   bf16 [E][2I][H]: rows 0..I-1 the gate, I..2I-1 the up projection
  *   down      bf16 [E][H][I]
  *   offsets   int32 [E+1] on the device, as for moeq_grouped_mm
- *   gu_saved  NULL, or bf16 [M][2I] for g | u, which the backward pass takes
+ *   gu_saved  NULL, or fp32 [M][2I] for g | u, which the backward pass takes
  *   workspace of moeq_grouped_ffn_workspace_bytes(M, E, H, I), 16-byte aligned
- * g, u and the sums are fp32; h is rounded to bf16 for the down product, and g
- * and u are where they are saved.  The same bits from run to run.  Rows of out
- * and gu_saved outside [offsets[0], offsets[E]) are not written, and such rows
+ * g, u and the sums are fp32; h is rounded to bf16 for the down product.  The
+ * same bits from run to run.  Rows of out and gu_saved outside [offsets[0], offsets[E]) are not written, and such rows
  * of x never reach a result.  Alignment, overlaps and offsets that do not
  * ascend as for moeq_grouped_mm.  MOEQ_ESHAPE unless moeq_grouped_mm and
  * moeq_grouped_mm_grad_input take both products (H and I multiples of 8, 4*I*H
@@ -560,7 +559,7 @@ moeq_status moeq_grouped_mm_fp8(const moeq_qweight *x, const moeq_qweight *w, co
  */
 size_t moeq_grouped_ffn_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t I);
 moeq_status moeq_grouped_ffn(const uint16_t *x_bf16, const uint16_t *gate_up_bf16, const uint16_t *down_bf16,
-                             const int32_t *offsets, int32_t M, int32_t E, int32_t H, int32_t I, uint16_t *gu_saved,
+                             const int32_t *offsets, int32_t M, int32_t E, int32_t H, int32_t I, float *gu_saved,
                              uint16_t *out_bf16, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
@@ -582,7 +581,7 @@ moeq_status moeq_grouped_ffn(const uint16_t *x_bf16, const uint16_t *gate_up_bf1
 size_t moeq_grouped_ffn_backward_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t I);
 moeq_status moeq_grouped_ffn_backward(const uint16_t *grad_out_bf16, const uint16_t *x_bf16,
                                       const uint16_t *gate_up_bf16, const uint16_t *down_bf16, const int32_t *offsets,
-                                      const uint16_t *gu_saved, int32_t M, int32_t E, int32_t H, int32_t I,
+                                      const float *gu_saved, int32_t M, int32_t E, int32_t H, int32_t I,
                                       int32_t dtype, uint16_t *grad_x_bf16, void *grad_gate_up, void *grad_down,
                                       void *workspace, size_t workspace_bytes, void *stream);
 

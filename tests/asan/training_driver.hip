@@ -43,8 +43,8 @@ hipError_t launch_grouped_mm_grad_weight(const GroupedArgs& g, bool, hipStream_t
 }
 int64_t clip_partials(int32_t) { return 1; }
 hipError_t launch_clip(const moeq_grad*, int32_t, double, float*, double*, hipStream_t) { return hit(); }
-hipError_t launch_glu(const GroupedArgs&, uint16_t*, hipStream_t) { return hit(); }
-hipError_t launch_glu_backward(const GroupedArgs&, const uint16_t*, uint16_t*, hipStream_t) { return hit(); }
+hipError_t launch_glu(const GroupedArgs&, float*, hipStream_t) { return hit(); }
+hipError_t launch_glu_backward(const GroupedArgs&, const float*, uint16_t*, hipStream_t) { return hit(); }
 hipError_t launch_quantize_fp8(const uint16_t*, uint8_t*, float*, int32_t, int32_t, int32_t, bool, hipStream_t) {
   return hit();
 }
@@ -84,7 +84,7 @@ static void feed_forward() {
     for (const int32_t E : {INT_MIN, 0, 1, 64, 1024, 1025, INT_MAX})
       for (const int32_t H : kEdges)
         for (const int32_t I : kEdges) {
-          const moeq_status st = moeq_grouped_ffn(at(1), at(2), at(3), at<int32_t>(4), M, E, H, I, at(5), at(6), at<void>(7),
+          const moeq_status st = moeq_grouped_ffn(at(1), at(2), at(3), at<int32_t>(4), M, E, H, I, at<float>(5), at(6), at<void>(7),
                                                   SIZE_MAX, nullptr);
           const size_t need = moeq_grouped_ffn_workspace_bytes(M, E, H, I);
           const size_t back = moeq_grouped_ffn_backward_workspace_bytes(M, E, H, I);
@@ -95,7 +95,7 @@ static void feed_forward() {
             EXPECT(need >= (size_t)M * I * 2 && back >= (size_t)M * I * 6, true);
             EXPECT(moeq_grouped_ffn(at(1), at(2), at(3), at<int32_t>(4), M, E, H, I, nullptr, at(6), at<void>(7), need - 1,
                                     nullptr), MOEQ_EWORKSPACE);
-            EXPECT(moeq_grouped_ffn_backward(at(1), at(2), at(3), at(4), at<int32_t>(5), at(6), M, E, H, I, MOEQ_DTYPE_FP32,
+            EXPECT(moeq_grouped_ffn_backward(at(1), at(2), at(3), at(4), at<int32_t>(5), at<float>(6), M, E, H, I, MOEQ_DTYPE_FP32,
                                              at(7), at<void>(8), at<void>(9), at<void>(10), back, nullptr), MOEQ_OK);
           }
         }
@@ -104,7 +104,7 @@ static void feed_forward() {
          MOEQ_OK);
   EXPECT(launches - before, 2);
   before = launches;
-  EXPECT(moeq_grouped_ffn_backward(at(1), at(2), at(3), at(4), at<int32_t>(5), at(6), 8, 2, 16, 24, MOEQ_DTYPE_BF16, at(7),
+  EXPECT(moeq_grouped_ffn_backward(at(1), at(2), at(3), at(4), at<int32_t>(5), at<float>(6), 8, 2, 16, 24, MOEQ_DTYPE_BF16, at(7),
                                    at<void>(8), at<void>(9), at<void>(10), 1 << 20, nullptr), MOEQ_OK);
   EXPECT(launches - before, 4);
   before = launches;   // no rows: the weights' gradients are zeros

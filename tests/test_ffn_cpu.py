@@ -20,7 +20,7 @@ def _t(*shape, dtype=BF):
 
 
 def test_binding_refuses():
-    x, w1, w2, off, gu = _t(5, 16), _t(2, 48, 16), _t(2, 16, 24), torch.zeros(3, dtype=torch.int32), _t(5, 48)
+    x, w1, w2, off, gu = _t(5, 16), _t(2, 48, 16), _t(2, 16, 24), torch.zeros(3, dtype=torch.int32), _t(5, 48, dtype=torch.float32)
     f, b = moeq.moeq_grouped_ffn, moeq.moeq_grouped_ffn_backward
     bad = [
         (ValueError, f, (x[0], w1, w2, off), {}),
@@ -34,8 +34,8 @@ def test_binding_refuses():
         (TypeError, f, (x.float(), w1, w2, off), {}),
         (TypeError, f, (x, w1.half(), w2, off), {}),
         (ValueError, f, (x, w1, w2, off), dict(out=_t(4, 16))),
-        (ValueError, f, (x, w1, w2, off), dict(gu=_t(5, 24))),
-        (TypeError, f, (x, w1, w2, off), dict(gu=_t(5, 48, dtype=torch.float32))),
+        (ValueError, f, (x, w1, w2, off), dict(gu=_t(5, 24, dtype=torch.float32))),
+        (TypeError, f, (x, w1, w2, off), dict(gu=_t(5, 48))),
         (ValueError, b, (_t(4, 16), x, w1, w2, off, gu), {}),
         (ValueError, b, (x, x, w1, w2, off, _t(5, 24)), {}),
         (TypeError, b, (x, x, w1, w2, off, gu), dict(dtype=torch.float16)),

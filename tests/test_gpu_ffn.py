@@ -6,7 +6,7 @@ most L 2^-23 of the sum of their magnitudes (the matrix cores may truncate).
 exp and the reciprocal are off by some units of 2^-23, exp's argument by |g|
 more; every formula below has at most ten operations, so kOps = 16 of them are
 allowed.  A value stored in bf16 is off by 2^-8 of itself.  With s the sigmoid:
-  g, u     |d| <= H 2^-23 mag, and 2^-8 where saved
+  g, u     |d| <= H 2^-23 mag (saved as they are)
   h        |u s (1 + g (1 - s))| dg + |g s| du + (kOps + |g|) 2^-23 |h|, then 2^-8
   dg, du   the same with dh's error (H 2^-23 mag) and the sum's two terms apart
   out, grad_x and the weights' gradients: the products of the operands' errors
@@ -62,7 +62,7 @@ def _check_forward(x, w1, w2, off, y, gu):
     want = pre_activations(xs, a, off)
     err = H * SUM * pre_activations(np.abs(xs), np.abs(a), off)
     if gu is not None:
-        _near(gu, want, HALF * np.abs(want) + err * (1 + HALF), "gu")
+        _near(gu, want, err, "gu")
     g, u = np.split(want, 2, axis=1)
     eg, eu = np.split(err, 2, axis=1)
     s, h = sigmoid(g), hidden(want)
@@ -107,7 +107,7 @@ def test_block_and_gradients(rows, H, I):
     say(f"ffn {rows} H={H} I={I}")
     x, dy, w1, w2, off, doff = _case(*ROWS[rows], H, I)
     M = x.shape[0]
-    y, gu = torch.full((M, H), 7.0, dtype=BF16, device=DEV), torch.full((M, 2 * I), 7.0, dtype=BF16, device=DEV)
+    y, gu = torch.full((M, H), 7.0, dtype=BF16, device=DEV), torch.full((M, 2 * I), 7.0, dtype=F32, device=DEV)
     got = moeq.moeq_grouped_ffn(x, w1, w2, doff, out=y, gu=gu)
     assert got[0] is y and got[1] is gu
     _check_forward(x, w1, w2, off, y, gu)
@@ -151,8 +151,8 @@ def test_far_gates():
     off = torch.tensor([0, 8], dtype=torch.int32, device=DEV)
     y, gu = moeq.moeq_grouped_ffn(x, w1.to(BF16), w2.to(BF16), off, save=True)
     want = hidden(_f64(gu))[:, 0]
-    # the roundings of the saved g, of h and of the output
-    assert np.all(np.abs(_f64(y)[:, 0] - want) <= 3.1 * HALF * np.abs(want) + 1e-30)
+    # the roundings of h and of the output
+    assert np.all(np.abs(_f64(y)[:, 0] - want) <= 2.1 * HALF * np.abs(want) + 1e-30)
     dx, dw1, dw2 = moeq.moeq_grouped_ffn_backward(torch.ones_like(x), x, w1.to(BF16), w2.to(BF16), off, gu)
     assert all(torch.isfinite(t).all() for t in (dx, dw1, dw2))
 
@@ -160,7 +160,7 @@ def test_far_gates():
 def test_no_rows():
     say("ffn no rows at all")
     off = torch.zeros(3, dtype=torch.int32, device=DEV)
-    x, gu = torch.empty((0, 16), dtype=BF16, device=DEV), torch.empty((0, 48), dtype=BF16, device=DEV)
+    x, gu = torch.empty((0, 16), dtype=BF16, device=DEV), torch.empty((0, 48), dtype=F32, device=DEV)
     w1, w2 = torch.ones((2, 48, 16), dtype=BF16, device=DEV), torch.ones((2, 16, 24), dtype=BF16, device=DEV)
     assert moeq.moeq_grouped_ffn(x, w1, w2, off).shape == (0, 16)
     dx, dw1, dw2 = moeq.moeq_grouped_ffn_backward(x, x, w1, w2, off, gu)
@@ -177,7 +177,7 @@ def test_nothing_is_written_past_the_end(rows, H, I):
     say(f"ffn guarded {rows} H={H} I={I}")
     x, dy, w1, w2, off, doff = _case(GUARDED[rows], 0, 0, H, I, seed=2)
     M, E = x.shape[0], len(off) - 1
-    y, gu = Guarded((M, H), BF16), Guarded((M, 2 * I), BF16)
+    y, gu = Guarded((M, H), BF16), Guarded((M, 2 * I), F32)
     ws = Guarded((moeq.moeq_grouped_ffn_workspace_bytes(M, E, H, I),), U8)
     moeq.moeq_grouped_ffn(x, w1, w2, doff, out=y.t, gu=gu.t, workspace=ws.t)
     ref = moeq.moeq_grouped_ffn(x, w1, w2, doff, save=True)
@@ -201,7 +201,7 @@ def test_offsets_that_do_not_ascend_stay_inside(bad):
     say(f"ffn offsets {bad}")
     x, dy, w1, w2, _, _ = _case([20, 20, 20], 0, 0, 72, 40, seed=3)
     off = torch.tensor(bad, dtype=torch.int32, device=DEV)
-    y, gu = Guarded((60, 72), BF16, 1.0), Guarded((60, 80), BF16, 1.0)
+    y, gu = Guarded((60, 72), BF16, 1.0), Guarded((60, 80), F32, 1.0)
     ws, bw = (Guarded((n(60, 3, 72, 40),), U8) for n in (moeq.moeq_grouped_ffn_workspace_bytes,
                                                          moeq.moeq_grouped_ffn_backward_workspace_bytes))
     moeq.moeq_grouped_ffn(x, w1, w2, off, out=y.t, gu=gu.t, workspace=ws.t)

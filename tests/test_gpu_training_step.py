@@ -118,7 +118,7 @@ def test_two_streams_at_once():
 
 
 def test_block_past_32_bit_offsets():
-    """g | u of 4.9 GB: the last expert's rows come out as in a call of their own."""
+    """g | u of 9.8 GB: the last expert's rows come out as in a call of their own."""
     say("ffn past 32-bit offsets")
     M, H, I = 150_000, 8, 8192
     g = torch.Generator(device=DEV).manual_seed(5)
