@@ -364,15 +364,15 @@ __global__ __launch_bounds__(64 * kNWN * kNWM, kNWN * kNWM / 4) void fp8_rows_ke
 // formats' form.  A unit is two blocks of the contraction (256 bytes of a row).
 constexpr int kFewWaves = 4;
 
-template <bool kSplit>
+template <bool kSplit, int kC>
 __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g) {
-  constexpr int kCols = kSplit ? 16 : 16 * kFewWaves;   // of a workgroup
-  __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][64];
+  constexpr int kWave = 16 * kC, kCols = kSplit ? kWave : kWave * kFewWaves;   // columns of a wave, of a workgroup
+  __shared__ __attribute__((aligned(16))) f32x4 part[kSplit ? kFewWaves : 1][kC][64];
   int e, row0, nrows, ct;
   if (!find_tile(g, 16, (g.nout + kCols - 1) / kCols, e, row0, nrows, ct)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, grp = lane >> 4, nkb = g.nkb;
-  const int c0 = ct * kCols + (kSplit ? 0 : 16 * wave), ncols = min(16, g.nout - c0);
+  const int c0 = ct * kCols + (kSplit ? 0 : kWave * wave), ncols = min(kWave, g.nout - c0);
   if (!kSplit && ncols <= 0) return;   // (no barrier there)
   const __amdgpu_buffer_rsrc_t rx = buffer(static_cast<const char*>(g.x) + (int64_t)row0 * g.kc, (int64_t)nrows * g.kc);
   const __amdgpu_buffer_rsrc_t rw =
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g)
   const float* ws = g.ws + ((int64_t)e * fp8_blocks(g.nout) + c0 / kFp8Block) * nkb;
 
   struct Unit {
-    u32x4 w[2][2], x[2][2];
+    u32x4 w[kC][2][2], x[2][2];
     float s[2], t[2];
   };
   auto load = [&](Unit& v, int u) {
@@ -391,7 +391,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g)
       for (int k = 0; k < 2; ++k) {
         const int at = u * 256 + 128 * j + 64 * k + 16 * grp;
         const uint32_t off = at < g.kc ? (uint32_t)l16 * (uint32_t)g.kc + (uint32_t)at : kPast;
-        v.w[j][k] = buffer_load16(rw, off);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          v.w[c][j][k] = buffer_load16(rw, at < g.kc ? (uint32_t)(16 * c + l16) * (uint32_t)g.kc + (uint32_t)at : kPast);
         v.x[j][k] = buffer_load16(rx, off);
       }
       const int b = min(2 * u + j, nkb - 1);   // (past the end the codes are zeros)
@@ -399,17 +401,27 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g)
       v.t[j] = ws[b];
     }
   };
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[kC];
+#pragma unroll
+  for (int c = 0; c < kC; ++c) acc[c] = (f32x4){0.f, 0.f, 0.f, 0.f};
   auto use = [&](const Unit& v, int u) {
-    f32x4 r[2] = {mfma_fp8(v.w[0], v.x[0]), mfma_fp8(v.w[1], v.x[1])};
-    mfma_done(r[0]);
-    mfma_done(r[1]);
+    f32x4 r[kC][2];
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) r[c][j] = mfma_fp8(v.w[c][j], v.x[j]);
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mfma_done(r[c][j]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (2 * u + j < nkb) {
         const float s = v.s[j] * v.t[j];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(r[j][i], s, acc[i]);
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[c][i] = __builtin_fmaf(r[c][j][i], s, acc[c][i]);
       }
   };
   const int units = (nkb + 1) / 2;
@@ -427,19 +439,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_rows_kernel(Fp8Args g)
     u += kStep;
   }
   if constexpr (kSplit) {
-    part[wave][lane] = acc;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) part[wave][c][lane] = acc[c];
     __syncthreads();
     if (wave) return;
 #pragma unroll
-    for (int v = 1; v < kFewWaves; ++v) {
-      const f32x4 q = part[v][lane];
-      acc.x += q.x; acc.y += q.y; acc.z += q.z; acc.w += q.w;
-    }
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int v = 1; v < kFewWaves; ++v) {
+        const f32x4 q = part[v][c][lane];
+        acc[c].x += q.x; acc[c].y += q.y; acc[c].z += q.z; acc[c].w += q.w;
+      }
   }
   // the lane holds columns 4 (lane / 16) .. + 3 of row lane % 16
-  if (l16 < nrows && 4 * grp < ncols)
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + l16) * g.nout + c0 + 4 * grp) =
-        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+#pragma unroll
+  for (int c = 0; c < kC; ++c)
+    if (l16 < nrows && 16 * c + 4 * grp < ncols)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.out) + (int64_t)(row0 + l16) * g.nout + c0 + 16 * c + 4 * grp) =
+          make_uint2(pack_bf16x2(acc[c].x, acc[c].y), pack_bf16x2(acc[c].z, acc[c].w));
 }
 
 template <int kNWN, int kNWM, int kTN, int kTM, int kBufs>
@@ -451,25 +468,58 @@ hipError_t launch_rows(const Fp8Args& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_few_rows(const Fp8Args& g, hipStream_t s) {
-  const int64_t tiles = (g.nout + 15) / 16, slots = (int64_t)g.M / 16 + std::min(g.E, g.M);
-  if (g.nkb >= 4 * kFewWaves || slots * tiles < 4096)
-    fp8_few_rows_kernel<true><<<(unsigned)items_grid(slots * tiles), 64 * kFewWaves, 0, s>>>(g);
-  else
-    fp8_few_rows_kernel<false>
-        <<<(unsigned)items_grid(slots * ((tiles + kFewWaves - 1) / kFewWaves)), 64 * kFewWaves, 0, s>>>(g);
+template <bool kSplit, int kC>
+hipError_t launch_few_as(const Fp8Args& g, int64_t slots, hipStream_t s) {
+  constexpr int kCols = 16 * kC * (kSplit ? 1 : kFewWaves);
+  fp8_few_rows_kernel<kSplit, kC>
+      <<<(unsigned)items_grid(slots * ((g.nout + kCols - 1) / kCols)), 64 * kFewWaves, 0, s>>>(g);
   return hipGetLastError();
 }
 
-bool streams(const GroupedArgs& g) {
-  const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
-  // A grid holds less than 2^32 threads; beyond that the tiles serve.
-  return (g.M <= 4 * g.E || g.nout <= 16) && items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
+// A wave's share of the contraction has to be long enough to start on: up to
+// 2048 (16 blocks), four waves share an item only where there are few of them
+// (K = 2048, shared and not: 64 rows over 64 experts of 2048 columns 59 and 55 us,
+// 128 over 128 of 1536 85 and 71; 16 of them 15.4 and 16.0).  Past 2048 they
+// always do, and two blocks of 16 columns halve what is read of x, which tells
+// from two rows an expert on (E = 8, N = 28672, K = 4096, one and two blocks: 8
+// rows 152 and 158 us, 16 rows 170 and 161, 32 rows 187 and 166).
+hipError_t launch_few_rows(const Fp8Args& g, hipStream_t s) {
+  const int64_t slots = (int64_t)g.M / 16 + std::min(g.E, g.M);
+  if (g.nkb <= 16 && slots * ((g.nout + 15) / 16) >= 2048) return launch_few_as<false, 1>(g, slots, s);
+  if (g.nkb > 16 && g.M >= 2 * (int64_t)g.E) return launch_few_as<true, 2>(g, slots, s);
+  return launch_few_as<true, 1>(g, slots, s);
 }
 
+// Whether the weights stream past the rows.  us streamed and in tiles, the same
+// number of rows for each expert, weights from HBM:
+//   rows an expert                 1         2         4         8
+//     E = 8, N = 28672, K = 4096  152, 192  161, 192  166, 193  185, 195
+//     E = 8, N = K = 4096          29, 37    31, 37    32, 37    34, 37
+//     E = 32, N = K = 2880         54, 57    55, 57    57, 58    62, 58
+//     E = 128, N = 1536, K = 2048  71, 75    75, 76    80, 76    95, 77
+//     E = 64, N = K = 2048         55, 53    57, 53    59, 53    66, 53
+// so up to four rows, and two where the contraction is short.  Outputs of up to 16
+// columns are one item of the stream.
+// A grid holds less than 2^32 threads; beyond that the tiles serve.
+bool streams(const Fp8Args& g) {
+  const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
+  return (g.M <= (g.nkb > 16 ? 4 : 2) * (int64_t)g.E || g.nout <= 16) &&
+         items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
+}
+
+// Whether tiles of half the columns do better: where they leave fewer compute units
+// without work (in the last of the rounds over 256, as long as the rows are few and
+// the weights bound it; in the only round otherwise).  us in half and in whole tiles:
+//   8 experts, N = K = 4096, 8 / 128 rows each       36.8, 38.4   39.9, 46.4
+//   32 experts, N = K = 2880, 8 / 128 rows each      57.8, 62.9   82.4, 80.0
+//   8 experts, N = 28672, K = 4096, 8 / 128 rows     195, 201     236, 223
+//   64 experts, N = K = 2048, 8 / 128 rows each      57.5, 52.9   78.1, 63.7
 bool few_tiles(const GroupedArgs& g) {
-  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
-  return rows * ((g.nout + 255) / 256) <= 128;
+  const int64_t experts = std::min(g.E, g.M), each = g.M / experts;
+  const int64_t rows = std::max<int64_t>(1, (each + 255) / 256) * experts;
+  const int64_t whole = rows * ((g.nout + 255) / 256), half = rows * ((g.nout + 127) / 128);
+  if (each <= 64) return (half + 255) / 256 < 2 * ((whole + 255) / 256);
+  return whole <= 128;
 }
 
 }  // namespace

@@ -288,11 +288,24 @@ hipError_t launch_shape(const OrthoProduct& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The largest tiles of 256, 128 or 64 that give each of 256 compute units one.
+// us of five steps with tiles of 64, of 128, of 256 throughout:
+//   1 x [1024, 1024] 140, 267, 428      16 x [1024, 1024]  797,  634,  585
+//   1 x [2048, 2048] 422, 474, 677      4 x [2048, 4096]  2105, 1749, 1450
+//   32 x [512, 512]  303, 270, 336      64 x [1024, 2048] 5098, 3827, 3203
+//   1 x [3000, 3000] 1372, 1081, 1094   1 x [4096, 4096]  2329, 1938, 1596
+// For tiles of 128 a symmetric product's half is counted (1 x [2048, 2048], all of
+// them and half, 474 and 410, 4 x [1024, 1024] 294 and 260), for tiles of 256 all:
+// their half is 160 for 16 x [1024, 1024], where tiles of 128 take longer (602, 580).
 template <Then kThen, bool kAT, bool kBT>
 hipError_t launch_product(const OrthoProduct& g, hipStream_t s) {
-  auto tiles = [&](int size) { return (int64_t)g.E * ((g.rows + size - 1) / size) * ((g.cols + size - 1) / size); };
-  if (g.rows <= 64 || g.cols <= 64 || tiles(128) < 256) return launch_shape<kThen, kAT, kBT, 2, 2, 1, 1, 3, 3>(g, s);
-  if (tiles(256) < 256) return launch_shape<kThen, kAT, kBT, 2, 2, 2, 2, 2, 2>(g, s);
+  auto tiles = [&](int size, bool half) {
+    const int64_t nr = (g.rows + size - 1) / size;
+    return g.E * (half ? triangle(nr) : nr * ((g.cols + size - 1) / size));
+  };
+  if (g.rows <= 64 || g.cols <= 64 || tiles(128, symmetric(kThen)) < 256)
+    return launch_shape<kThen, kAT, kBT, 2, 2, 1, 1, 3, 3>(g, s);
+  if (tiles(256, false) < 256) return launch_shape<kThen, kAT, kBT, 2, 2, 2, 2, 2, 2>(g, s);
   return launch_shape<kThen, kAT, kBT, 4, 2, 2, 4, 3, 2>(g, s);
 }
 

@@ -168,6 +168,27 @@ def test_product(rows, N, K):
     assert _untouched(y, off)
 
 
+@pytest.mark.parametrize("sizes", [[1, 0, 2], [5, 0, 4], [17, 1, 0, 0, 0], [1] * 7 + [21] + [0] * 30, [2] * 64])
+@pytest.mark.parametrize("N,K", [(8, 2064), (72, 2064), (264, 2576), (520, 400)])
+def test_few_rows_an_expert(sizes, N, K):
+    """Shares of the contraction with and without a last block, one and two
+    blocks of columns at a time, more than 16 rows of an expert."""
+    say(f"fp8 few rows {len(sizes)} experts, {sum(sizes)} rows N={N} K={K}")
+    xq, wq, off, doff = _operands(sizes, 0, 0, N, K, seed=8)
+    y = Guarded((xq.rows, N), BF16)
+    moeq.moeq_grouped_mm_fp8(xq, wq, doff, out=y.t)
+    y.check("out")
+    _check_product(y.t, xq, wq, off)
+
+
+@pytest.mark.parametrize("rows", [5, 33, 64])
+@pytest.mark.parametrize("E,N", [(3, 264), (33, 2056)])
+def test_tiles_of_few_rows(rows, E, N):
+    say(f"fp8 tiles of few rows E={E} rows={rows} N={N}")
+    xq, wq, off, doff = _operands([rows] * E, 0, 0, N, 272, seed=9)
+    _check_product(moeq.moeq_grouped_mm_fp8(xq, wq, doff), xq, wq, off)
+
+
 @pytest.mark.parametrize("sizes", [[3], [300], [2, 70, 0, 500]])
 @pytest.mark.parametrize("N,K", [(40, 8336), (264, 16400), (2600, 1040)])
 def test_long_contractions_and_many_columns(sizes, N, K):
