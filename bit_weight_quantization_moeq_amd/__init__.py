@@ -1,6 +1,8 @@
 """moeq: NF4 / row-wise int8 / MXFP4 quantization of fused MoE expert tensors,
 the routed experts forward straight from the packed storage, products grouped
-by expert with their gradients, and gradient clipping, on MI355X (gfx950).
+by expert with their gradients (bf16, MXFP4, block-scaled FP8), the gated
+feed-forward block over them forward and backward, gradient clipping and
+orthogonalised updates, on MI355X (gfx950).
 
 This module is a thin ctypes binding over ``libmoeq.so`` (declared in
 ``include/moeq.h``): it marshals torch tensors into device pointers and the
@@ -1226,8 +1228,10 @@ def moeq_orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=N
     batch ``[E, N, K]``) divided by its norm and taken through ``steps``
     Newton-Schulz steps ``X <- a X + (b A + c A A) X``, ``A = X X^T``, with
     ``coefficients`` ``(a, b, c)`` for all steps or one triple for each.  Returns
-    bf16 of ``g``'s shape.  Working matrices are fp16 with fp32 sums; a matrix of
-    zeros stays one, an infinity or a NaN makes its own matrix NaN."""
+    bf16 of ``g``'s shape.  Working matrices are fp16 with fp32 sums, whose
+    rounding grows in directions that a matrix lacks (full rank 0.2 % off after
+    five steps, rank one 10 %); a matrix of zeros stays one, an infinity or a NaN
+    makes its own matrix NaN."""
     if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
         raise ValueError("g must be a [N, K] or [E, N, K] tensor")
     if g.dtype not in _GRAD_DTYPES:

@@ -17,6 +17,14 @@
 // pass (in bf16, half the bytes, their rounding would be as large again as the
 // gradients' own: 3.5e-3 of grad_down instead of 2.4e-3).  h, dg and du are
 // rounded to bf16, because the next product's matrix instructions take bf16.
+//
+// Measured (median us of a kernel): 16384 rows, E = 8, H = 4096, I = 14336:
+// gate_up with silu(g) u 3340 (1.15 PFLOP/s, matrix cores 70 % busy at the 1.59
+// GHz that the card's power leaves), down 1690.  32768 rows, E = 64, H = 2048,
+// I = 1024, for training: gate_up 320 (0.86 PFLOP/s, 47 % busy at 2.0 GHz; 8 to
+// 32 steps of contraction a tile, whose first copies and stores nothing covers),
+// down's input gradient 230 (its epilogue reads and writes 580 MB), the rest of
+// the backward pass 270 + 170 + 280.  One token over 64 experts: weights at HBM's rate.
 #include "grouped_tile.h"
 
 #include "ffn.h"

@@ -13,7 +13,10 @@
 // units elsewhere.  Blocks whose amax lies far from 1 are taken times 2^64 or
 // 2^-64 first, so that none of this leaves fp32's normal range.
 //
-// Bound by memory: bf16 in (or out) 2 bytes and codes 1 byte a value.
+// Bound by memory: bf16 in (or out) 2 bytes and codes 1 byte a value.  Measured,
+// [32, 5760, 2880] in tiles: 287 us there (5.6 TB/s, part of the input from the
+// memory-side cache) and 356 back (4.5 TB/s); a copy reaches 4.7 to 4.9.  64 rows
+// of 2880: 3 us each, a launch's latency.
 #include "fp8.h"
 
 namespace moeq {

@@ -19,6 +19,12 @@
 //
 // Tiles, LDS layout and copies are those of grouped_tile.h; a step of 128 bytes
 // is one block.
+//
+// Measured: 32768 rows over 8 experts of [28672, 4096] 3.8 ms, 2.03 PFLOP/s,
+// matrix cores 51 % busy at 1.77 GHz.  A step's matrix instructions take as long
+// as the LDS reads of their operands, and the copies into LDS come on top (without
+// them 3.15 ms, without LDS 2.54).  8192 rows over 128 experts of [1536, 2048]:
+// 100 us, and 64 rows over 32 of [5760, 2880] 83: the weights from HBM.
 #include "grouped_tile.h"
 
 #include "fp8.h"
@@ -509,7 +515,8 @@ bool streams(const Fp8Args& g) {
 
 // Whether tiles of half the columns do better: where they leave fewer compute units
 // without work (in the last of the rounds over 256, as long as the rows are few and
-// the weights bound it; in the only round otherwise).  us in half and in whole tiles:
+// the weights bound it; in the only round otherwise), up to 8 rounds, past which a
+// part of one is little.  us in half and in whole tiles:
 //   8 experts, N = K = 4096, 8 / 128 rows each       36.8, 38.4   39.9, 46.4
 //   32 experts, N = K = 2880, 8 / 128 rows each      57.8, 62.9   82.4, 80.0
 //   8 experts, N = 28672, K = 4096, 8 / 128 rows     195, 201     236, 223
@@ -518,7 +525,7 @@ bool few_tiles(const GroupedArgs& g) {
   const int64_t experts = std::min(g.E, g.M), each = g.M / experts;
   const int64_t rows = std::max<int64_t>(1, (each + 255) / 256) * experts;
   const int64_t whole = rows * ((g.nout + 255) / 256), half = rows * ((g.nout + 127) / 128);
-  if (each <= 64) return (half + 255) / 256 < 2 * ((whole + 255) / 256);
+  if (each <= 64 && whole <= 8 * 256) return (half + 255) / 256 < 2 * ((whole + 255) / 256);
   return whole <= 128;
 }
 

@@ -189,6 +189,23 @@ def test_tiles_of_few_rows(rows, E, N):
     _check_product(moeq.moeq_grouped_mm_fp8(xq, wq, doff), xq, wq, off)
 
 
+def test_millions_of_tiles():
+    """Rows for which smaller tiles would do, in so many of them that their grid
+    would not hold: 1024 experts of 5 rows, 2^20 columns."""
+    say("fp8 millions of tiles")
+    E, N, K, each = 1024, 1 << 20, 16, 5
+    g = torch.Generator(device=DEV).manual_seed(10)
+    codes = torch.randint(-4, 5, (1, N, K), generator=g, device=DEV).float().to(F8)
+    wq = moeq.QWeight(moeq.FMT_FP8_TILE, E, N, K, codes.repeat(E, 1, 1), torch.ones((E, N // 128, 1), device=DEV))
+    wq.scales *= torch.exp2(torch.arange(E, device=DEV) % 5).reshape(E, 1, 1)
+    xc = torch.randint(-4, 5, (1, each * E, K), generator=g, device=DEV).float()
+    xq = moeq.QWeight(moeq.FMT_FP8_ROW, 1, each * E, K, xc.to(F8), torch.ones((1, each * E, 1), device=DEV))
+    y = moeq.moeq_grouped_mm_fp8(xq, wq, torch.arange(0, each * E + 1, each, dtype=torch.int32, device=DEV))
+    w = codes[0].float().t().contiguous()
+    for e in (0, 1, 511, 1023):
+        assert torch.equal(y[each * e:each * e + each], ((xc[0, each * e:each * e + each] @ w) * 2.0 ** (e % 5)).to(BF16))
+
+
 @pytest.mark.parametrize("sizes", [[3], [300], [2, 70, 0, 500]])
 @pytest.mark.parametrize("N,K", [(40, 8336), (264, 16400), (2600, 1040)])
 def test_long_contractions_and_many_columns(sizes, N, K):
