@@ -35,7 +35,8 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
-__device__ __forceinline__ float glu(float g, float u) { return g * u * sigmoid(g); }
+// (u last: g u may leave fp32's range where silu(g) u does not)
+__device__ __forceinline__ float glu(float g, float u) { return g * sigmoid(g) * u; }
 
 // gate_up product of a tile: rows row0 .. + nrows, columns c0 .. of h.
 template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
@@ -177,9 +178,9 @@ __device__ __forceinline__ void glu_backward_tile(char* smem, const GroupedArgs&
           for (int j = 0; j < 2; ++j) {
             const float gv = gs[2 * i + j], uv = us[2 * i + j];
             const float s = sigmoid(gv), d = dh[2 * i + j];
-            o[0][j] = d * uv * (s * (1.0f + gv * (1.0f - s)));
+            o[0][j] = d * (s * (1.0f + gv * (1.0f - s))) * uv;   // (u last, as in glu)
             o[1][j] = d * (gv * s);
-            o[2][j] = gv * uv * s;
+            o[2][j] = gv * s * uv;
           }
           dgv[i] = pack_bf16x2(o[0][0], o[0][1]);
           duv[i] = pack_bf16x2(o[1][0], o[1][1]);
