@@ -1227,8 +1227,9 @@ def moeq_orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=N
     """Orthogonalised update: each matrix of ``g`` (bf16 or fp32, ``[N, K]`` or a
     batch ``[E, N, K]``) divided by its norm and taken through ``steps``
     Newton-Schulz steps ``X <- a X + (b A + c A A) X``, ``A = X X^T``, with
-    ``coefficients`` ``(a, b, c)`` for all steps or one triple for each.  Returns
-    bf16 of ``g``'s shape.  Working matrices are fp16 with fp32 sums, whose
+    ``coefficients`` ``(a, b, c)`` for all steps or one triple for each, of any
+    size that keeps the singular values below 15.9.  Returns bf16 of ``g``'s
+    shape.  Working matrices are fp16 with fp32 sums, whose
     rounding grows in directions that a matrix lacks (full rank 0.2 % off after
     five steps, rank one 10 %); a matrix of zeros stays one, an infinity or a NaN
     makes its own matrix NaN."""

@@ -14,8 +14,8 @@
 // 1024, five steps: 1.3e-3 off before the output's rounding, bf16 working
 // matrices 1.1e-2), and its products run at the same rate.  Powers of two keep
 // the entries in fp16's normal range: X times 2^s, s = floor(log2(sqrt(m))) with
-// m the longer side, so that entries of an orthogonal matrix are around 1, and
-// A and P times 2^8.  Sums are fp32, the norm's fp64.  What the rounding adds to
+// m the longer side, so that entries of an orthogonal matrix are around 1, A times
+// 2^8, and P times 2^8 or less (Poly).  Sums are fp32, the norm's fp64.  What the rounding adds to
 // directions that the matrix lacks grows by a from step to step as small singular
 // values do: with a = 3.4445, a matrix of rank one in 512 is 10 % off after five.
 //
@@ -24,6 +24,8 @@
 // the card's power leaves; half of A and P is computed), start 650.  64 of [2048,
 // 1024] 190, 122, 270 (1.0 PFLOP/s): 640 tiles of half the products and 1024 of the
 // whole ones, of 16 to 32 steps, whose first copies and stores nothing covers.
+#include <cmath>
+
 #include "grouped_tile.h"
 
 #include "ortho.h"
@@ -31,7 +33,23 @@
 namespace moeq {
 namespace {
 
-constexpr int kShift = 8;   // A and P are stored times 2^kShift
+constexpr int kShift = 8;   // A is stored times 2^kShift
+
+// A step's polynomial as its kernels take it: P times 2^k from A times 2^8, and
+// what takes a product with it back.  No entry of P is larger than its 2-norm, the
+// largest |a + b s^2 + c s^4| of a singular value s (0 among them): at most |a| + |b|
+// + |c| up to s = 1, and beyond 1, where the step's result keeps s below 16, below
+// 16 itself.  k = 8 as long as 2^8 (|a| + |b| + |c|) <= 2^15, half of fp16's range;
+// past that, which a alone reaches at 128, as much less as it takes.
+struct Poly {
+  float a, b, c, down;
+};
+Poly poly_of(const float* abc) {
+  const double sum = std::fabs((double)abc[0]) + std::fabs((double)abc[1]) + std::fabs((double)abc[2]);
+  int k = kShift;
+  while (std::ldexp(sum, k) > 0x1p15) --k;
+  return {std::ldexp(abc[0], k), std::ldexp(abc[1], k - kShift), std::ldexp(abc[2], k - 2 * kShift), std::ldexp(1.0f, -k)};
+}
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
 __device__ __forceinline__ float value(const uint16_t* p) { return bf16_value(*p); }
@@ -333,7 +351,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 struct OrthoSteps {
-  float abc[kOrthoMaxSteps][3];
+  Poly poly[kOrthoMaxSteps];
 };
 constexpr int kBatch = 4;
 
@@ -408,7 +426,7 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
     }
     if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // (all loads at once would not fit the registers)
   }
-  const float up = (float)(1 << kShift), down = 1.0f / up, gram_times = up / scale / scale;
+  const float gram_times = (float)(1 << kShift) / scale / scale;
   char* mine = turn[wave];
   f16x4 p16[kNB][kNB];
   // P X of column block b
@@ -480,7 +498,7 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
       }
     __syncthreads();   // (before the next step's sums)
     // (2^8 A)(2^8 A): a symmetric matrix's block (k, i) is the first operand's (i, k)
-    const float ca = table.abc[k][0] * up, cb = table.abc[k][1], cc = table.abc[k][2] * down;
+    const Poly c = table.poly[k];
 #pragma unroll
     for (int i = 0; i < kNB; ++i)
 #pragma unroll
@@ -491,7 +509,7 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
         mfma_done(v);
 #pragma unroll
         for (int z = 0; z < 4; ++z)
-          p16[i][j][z] = (_Float16)((i == j && 4 * grp + z == l16 ? ca : 0.f) + (cb * (float)a16[i][j][z] + cc * v[z]));
+          p16[i][j][z] = (_Float16)((i == j && 4 * grp + z == l16 ? c.a : 0.f) + (c.b * (float)a16[i][j][z] + c.c * v[z]));
       }
     if (k + 1 >= steps) break;
 #pragma unroll
@@ -501,7 +519,7 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
 #pragma unroll
       for (int i = 0; i < kNB; ++i)
 #pragma unroll
-        for (int z = 0; z < 4; ++z) x[i][b][z] = (_Float16)(y[i][z] * down);
+        for (int z = 0; z < 4; ++z) x[i][b][z] = (_Float16)(y[i][z] * c.down);
 #pragma unroll
       for (int i = 0; i < kNB; ++i) asm volatile("" : "+v"(x[i][b]));
       if (b % 4 == 3) __builtin_amdgcn_sched_barrier(0);
@@ -509,7 +527,7 @@ __global__ __launch_bounds__(64 * kNW) void ortho_few_kernel(const T* g, int32_t
   }
   // (addresses made anew, not kept from the loads through all steps)
   const __amdgpu_buffer_rsrc_t to = buffer(reinterpret_cast<const char*>(out), size * 2);
-  const float last = down / scale;
+  const float last = table.poly[steps - 1].down / scale;
   int c0 = 16 * wave + l16, r0 = 4 * grp;
   asm volatile("" : "+v"(c0), "+v"(r0));
 #pragma unroll
@@ -579,7 +597,7 @@ hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p,
   while (shift < 15 && (int64_t(1) << (2 * (shift + 1))) <= p.m) ++shift;
   if (few(p)) {
     OrthoSteps table = {};
-    for (int i = 0; i < 3 * steps; ++i) table.abc[i / 3][i % 3] = coefficients[i];
+    for (int i = 0; i < steps; ++i) table.poly[i] = poly_of(coefficients + 3 * i);
     const float scale = (float)(1 << shift);
     const uint16_t* g16 = static_cast<const uint16_t*>(grad);
     const float* g32 = static_cast<const float*>(grad);
@@ -593,22 +611,21 @@ hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p,
   double* partial = reinterpret_cast<double*>(ws + p.partial);
   _Float16 *x = reinterpret_cast<_Float16*>(ws + p.x), *y = reinterpret_cast<_Float16*>(ws + p.y);
   _Float16 *a = reinterpret_cast<_Float16*>(ws + p.a), *poly = reinterpret_cast<_Float16*>(ws + p.p);
-  const float up = (float)(1 << kShift);
   hipError_t e = fp32 ? launch_start(static_cast<const float*>(grad), p, (double)(1 << shift), partial, x, s)
                       : launch_start(static_cast<const uint16_t*>(grad), p, (double)(1 << shift), partial, x, s);
   const int64_t sx = (int64_t)p.N * p.xc, sa = (int64_t)p.n * p.nc;
   for (int i = 0; i < steps && e == hipSuccess; ++i) {
-    const float* k = coefficients + 3 * i;
+    const Poly c = poly_of(coefficients + 3 * i);
     OrthoProduct gram = {x, x, a, p.E, p.n, p.n, p.m, p.xc, p.xc, p.nc, sx, sx, sa};
-    gram.times = up / (float)(1 << shift) / (float)(1 << shift);
+    gram.times = (float)(1 << kShift) / (float)(1 << shift) / (float)(1 << shift);
     e = p.tall ? launch_product<Then::kGram, true, true>(gram, s) : launch_product<Then::kGram, false, false>(gram, s);
     if (e != hipSuccess) break;
     // (2^8 A)(2^8 A): A is symmetric, so its rows serve as its columns
     OrthoProduct square = {a, a, poly, p.E, p.n, p.n, p.n, p.nc, p.nc, p.nc, sa, sa, sa};
     square.a16 = a;
-    square.a = k[0] * up;
-    square.b = k[1];
-    square.c = k[2] / up;
+    square.a = c.a;
+    square.b = c.b;
+    square.c = c.c;
     e = launch_product<Then::kPoly, false, false>(square, s);
     if (e != hipSuccess) break;
     const bool last = i + 1 == steps;
@@ -621,12 +638,12 @@ hipError_t launch_orthogonalize(const void* grad, bool fp32, const OrthoPlan& p,
       apply.sw = sx;
       apply.sx = sa;
     }
-    apply.times = 1.0f / up;
+    apply.times = c.down;
     if (last) {
       apply.out = out;
       apply.ldo = p.K;
       apply.so = (int64_t)p.N * p.K;
-      apply.times = 1.0f / up / (float)(1 << shift);
+      apply.times = c.down / (float)(1 << shift);
       e = p.tall ? launch_product<Then::kOut, false, false>(apply, s) : launch_product<Then::kOut, true, false>(apply, s);
     } else {
       e = p.tall ? launch_product<Then::kApply, false, false>(apply, s) : launch_product<Then::kApply, true, false>(apply, s);

@@ -624,8 +624,9 @@ moeq_status moeq_clip_grad_norm(const moeq_grad *grads, int32_t count, double ma
  *   out_bf16      bf16 [E][N][K], 16-byte aligned
  *   workspace     of moeq_orthogonalize_workspace_bytes(E, N, K), 16-byte aligned
  * The norm is summed in fp64; X, A and the polynomial are kept in fp16, scaled by
- * powers of two, with fp32 sums, and the result is rounded to bf16, so
- * coefficients have to keep the singular values below about 2^4.  Directions that
+ * powers of two, with fp32 sums, and the result is rounded to bf16.  The
+ * coefficients may have any size, but have to keep every singular value below 15.9
+ * from step to step, or the result overflows.  Directions that
  * G lacks pick up fp16's rounding, which the steps raise with the small singular
  * values: with the usual coefficients a matrix of rank one in 512 is 10 % off after
  * five steps, one of full rank 0.2 %.  The same bits from run to run.  An infinity or a NaN makes its own matrix NaN.  MOEQ_EINVAL
