@@ -11,6 +11,7 @@ import subprocess
 
 import pytest
 
+from tests import test_gpu_ffn_large_tiles as ffn
 from tests import test_gpu_fp8_large_tiles as fp8
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,3 +60,10 @@ def test_large_fp8_tiles(launches, K):
     M, E = sum(fp8.SIZES), len(fp8.SIZES)
     for rows in (M, M + 8):
         assert [k[:2] for k in launches(f"fp8 {rows} {E} {fp8.N} {K}")] == [("fp8_rows_kernel", "4, 2, 4, 8, 2")]
+
+
+@pytest.mark.parametrize("H,I", ffn.SHAPES)
+def test_large_ffn_tiles(launches, H, I):
+    M, E = sum(ffn.SIZES) + 5, len(ffn.SIZES)
+    assert [k[:2] for k in launches(f"ffn {M} {E} {H} {I}")] == [("glu_kernel", "4, 2, 4, 3, 2")]
+    assert [k[:2] for k in launches(f"ffn_backward {M} {E} {H} {I}")] == [("glu_backward_kernel", "4, 2, 2, 4, 3, 2")]
