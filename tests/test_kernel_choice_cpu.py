@@ -13,6 +13,7 @@ import pytest
 
 from tests import test_gpu_ffn_large_tiles as ffn
 from tests import test_gpu_fp8_large_tiles as fp8
+from tests import test_gpu_orthogonalize_tiles as update
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -67,3 +68,13 @@ def test_large_ffn_tiles(launches, H, I):
     M, E = sum(ffn.SIZES) + 5, len(ffn.SIZES)
     assert [k[:2] for k in launches(f"ffn {M} {E} {H} {I}")] == [("glu_kernel", "4, 2, 4, 3, 2")]
     assert [k[:2] for k in launches(f"ffn_backward {M} {E} {H} {I}")] == [("glu_backward_kernel", "4, 2, 2, 4, 3, 2")]
+
+
+@pytest.mark.parametrize("shape", update.SHAPES)
+def test_update_tiles_of_128(launches, shape):
+    many = [k[1] for k in launches("orthogonalize {} {} {} 2".format(*shape)) if k[0] == "ortho_kernel"]
+    alone = [k[1] for k in launches("orthogonalize 1 {} {} 2".format(*shape[1:])) if k[0] == "ortho_kernel"]
+    # two steps of A, the polynomial and the result, the last one's in its own type
+    assert [a[0] for a in many] == [a[0] for a in alone] == list("012013")
+    assert all(a.endswith(", 2, 2, 2, 2, 2, 2") for a in many), many
+    assert all(a.endswith(", 2, 2, 1, 1, 3, 3") for a in alone), alone
