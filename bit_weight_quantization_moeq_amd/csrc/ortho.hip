@@ -118,9 +118,9 @@ __global__ __launch_bounds__(256) void ortho_scale_kernel(const T* g, int32_t N,
   const T* p = g + (int64_t)N * K * blockIdx.y;
   _Float16* o = x + (int64_t)N * xc * blockIdx.y;
   const uint32_t groups = xc / 8;
-  const int64_t total = (int64_t)N * groups;
+  const int64_t total = (int64_t)N * groups;   // (fits 32 bits: N K < 2^34, and N <= 2^20)
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = total < (int64_t(1) << 32) ? (int64_t)((uint32_t)i / groups) : i / groups;
+    const int64_t r = (uint32_t)i / groups;
     const int c = 8 * (int)(i - r * groups);
     float v[8];
     load8(p + r * K + c, K - c, wide, v);
