@@ -69,3 +69,12 @@ def test_small_and_large_in_turn(shape):
     for large in ((240.0, 0.0, 0.0), (240.0, -300.0, 100.0)):
         table = [(0.0625, 0.0, 0.0), large, (0.5, 0.0, 0.0)]
         _check(g, moeq.moeq_orthogonalize(g, 3, table), table)
+
+
+@pytest.mark.parametrize("shape", [(2, 20, 200), (2, 200, 20), (2, 40, 72)])
+def test_as_many_steps_as_there_may_be(shape):
+    """64 steps, the last with coefficients of its own."""
+    say(f"orthogonalize 64 steps {shape}")
+    g = torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(6), device=DEV)
+    table = [(1.5, -0.5, 0.0)] * 63 + [(200.0, -300.0, 110.0)]
+    _check(g, moeq.moeq_orthogonalize(g, 64, table), table)
