@@ -24,7 +24,8 @@
 // I = 1024, for training: gate_up 320 (0.86 PFLOP/s, 47 % busy at 2.0 GHz; 8 to
 // 32 steps of contraction a tile, whose first copies and stores nothing covers),
 // down's input gradient 230 (its epilogue reads and writes 580 MB), the rest of
-// the backward pass 270 + 170 + 280.  One token over 64 experts: weights at HBM's rate.
+// the backward pass 270 + 170 + 280.  One token over 64 experts: 100 MB of weights in
+// 21 us, 4.6 TB/s.
 #include "grouped_tile.h"
 
 #include "ffn.h"
@@ -311,27 +312,42 @@ hipError_t launch_glu_few_rows(const GroupedArgs& g, float* gu, hipStream_t s) {
 }
 
 // Whether the weights stream past the rows.  us of the whole block here and in
-// tiles, the same number of rows for each expert, weights from HBM:
+// tiles, the same number of rows for each expert, other weights from call to call (a
+// GB and more):
 //   rows an expert                       1         8        16        24
 //     E = 64, H = 2048, I = 1024   151, 179  166, 191  156, 177  223, 179
 //     E = 8, H = I = 4096          157, 177  161, 184  169, 190  226, 191
 //     E = 32, H = I = 2880         263, 267  283, 283  299, 283  426, 284
 //     E = 128, H = 2048, I = 768   208, 234  226, 251  230, 246  325, 249
-// so up to 16 rows, which are one pass over the weights; at 8 on average hardly
-// an expert has more.
+// so up to 16 rows, which are one pass over the weights.  Where the rows lie the
+// host does not know.  At 8 rows an expert on average, even, by Zipf's law (exponent
+// 1.1) and all in one expert, whose weights then pass many times:
+//     E = 64, H = 2048, I = 1024   166, 191  178, 189   92,  82
+//     E = 8, H = I = 4096          162, 185  167, 191   80,  66
+//     E = 32, H = I = 2880         283, 283  332, 315  158, 117
+//     E = 128, H = 2048, I = 768   220, 246  249, 266  123,  90
+// At 4 on average the stream is ahead by Zipf's law everywhere, and behind for one
+// expert's 32 rows of H = I = 2880 and more (86, 67).
 // A grid holds less than 2^32 threads; beyond that the tiles serve.
 bool streams(const GroupedArgs& g) {
   const int64_t items = ((int64_t)g.M / 16 + std::min(g.E, g.M)) * ((g.nout + 15) / 16);
   return g.M <= 8 * (int64_t)g.E && items_grid(items) * 64 * kFewWaves < (int64_t(1) << 32);
 }
 
-// Whether tiles of 128 columns of h (256 of dh) leave compute units without work:
-// those of half the columns then do better.  Eight rows in all, the gate_up
-// product in small and in large tiles: E = 64, H = 2048, I = 1024 32 and 37 us,
-// H = I = 2880 47 and 57 us (whole block).
-bool few_tiles(const GroupedArgs& g) {
+// Whether tiles of `cols` columns (128 of h, 256 of dh) leave compute units without
+// work: those of half the columns then do better.  us of the whole block, then of the
+// whole backward pass, in small and in large tiles, with the number of large ones:
+//   E = 1, 512 rows, H = 2048, I = 1024       16: 47, 61       8: 94, 110
+//   E = 8, 64 rows each, H = 2048, I = 1024   64: 38, 45      32: 83, 92
+//   E = 8, 512 each, H = 2048, I = 1024      128: 64, 76      64: 158, 173
+//   E = 4, 100 each, H = I = 4096            128: 110, 118    64: 267, 282
+//   E = 64, 64 each, H = 2048, I = 256       128: 58, 61      64: 126, 134
+//   E = 8, 256 each, H = I = 4096            256: 232, 219   128: 582, 593
+//   E = 64, 256 each, H = 2048, I = 512      256: 143, 136   128: 372, 367
+//   E = 64, 64 each, H = 2048, I = 1024      512: 186, 186   256: 391, 385
+bool few_tiles(const GroupedArgs& g, int32_t cols) {
   const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
-  return rows * ((g.nout + 127) / 128) <= 128;
+  return rows * ((g.nout + cols - 1) / cols) <= 128;
 }
 
 template <int kNWN, int kNWM, int kTM, int kBufsA, int kBufsB>
@@ -356,13 +372,12 @@ hipError_t launch_backward_tiles(const GroupedArgs& g, const float* gu, uint16_t
 
 hipError_t launch_glu(const GroupedArgs& g, float* gu, hipStream_t s) {
   if (streams(g)) return launch_glu_few_rows(g, gu, s);
-  if (few_tiles(g)) return launch_glu_tiles<2, 4, 2, 3, 3>(g, gu, s);
+  if (few_tiles(g, 128)) return launch_glu_tiles<2, 4, 2, 3, 3>(g, gu, s);
   return launch_glu_tiles<4, 2, 4, 3, 2>(g, gu, s);
 }
 
 hipError_t launch_glu_backward(const GroupedArgs& g, const float* gu, uint16_t* dgu, hipStream_t s) {
-  const int64_t experts = std::min(g.E, g.M), rows = std::max<int64_t>(1, (g.M / experts + 255) / 256) * experts;
-  if (rows * ((g.nout + 255) / 256) <= 128) return launch_backward_tiles<4, 2, 1, 4, 3, 3>(g, gu, dgu, s);
+  if (few_tiles(g, 256)) return launch_backward_tiles<4, 2, 1, 4, 3, 3>(g, gu, dgu, s);
   return launch_backward_tiles<4, 2, 2, 4, 3, 2>(g, gu, dgu, s);
 }
 
