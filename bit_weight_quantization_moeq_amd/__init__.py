@@ -1229,10 +1229,10 @@ def moeq_orthogonalize(g, steps=5, coefficients=(3.4445, -4.7750, 2.0315), out=N
     Newton-Schulz steps ``X <- a X + (b A + c A A) X``, ``A = X X^T``, with
     ``coefficients`` ``(a, b, c)`` for all steps or one triple for each, of any
     size that keeps the singular values below 15.9.  Returns bf16 of ``g``'s
-    shape.  Working matrices are fp16 with fp32 sums, whose
-    rounding grows in directions that a matrix lacks (after five steps full rank is
-    0.2 % off, rank 64 of 512 2 %, 16 4 %, 4 7 %, one 15 %); a matrix of zeros stays one, an infinity or a NaN
-    makes its own matrix NaN."""
+    shape.  Working matrices are fp16 with fp32 sums, whose rounding grows in
+    directions that a matrix lacks (after five steps full rank is 0.2 % off, rank
+    64 of 512 2 %, 16 4 %, 4 7 %, one 15 %); a matrix of zeros stays one, an
+    infinity or a NaN makes its own matrix NaN."""
     if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
         raise ValueError("g must be a [N, K] or [E, N, K] tensor")
     if g.dtype not in _GRAD_DTYPES:

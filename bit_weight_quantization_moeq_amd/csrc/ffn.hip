@@ -343,6 +343,7 @@ bool streams(const GroupedArgs& g) {
 //   E = 4, 100 each, H = I = 4096            128: 110, 118    64: 267, 282
 //   E = 64, 64 each, H = 2048, I = 256       128: 58, 61      64: 126, 134
 //   E = 8, 256 each, H = I = 4096            256: 232, 219   128: 582, 593
+//   E = 16, 64 each, H = I = 2048            256: 104, 108   128: 204, 212
 //   E = 64, 256 each, H = 2048, I = 512      256: 143, 136   128: 372, 367
 //   E = 64, 64 each, H = 2048, I = 1024      512: 186, 186   256: 391, 385
 bool few_tiles(const GroupedArgs& g, int32_t cols) {

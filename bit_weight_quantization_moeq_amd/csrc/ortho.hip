@@ -339,16 +339,17 @@ hipError_t launch_product(const OrthoProduct& g, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (adapters): one workgroup takes a matrix through all steps.  X stays
-// in registers (in the forms of 8 waves, past 2048 columns, which take all 256, 14 to
-// 32 of a lane's others go through scratch memory), in blocks of 16 x 16 as v_mfma_f32_16x16x16_f16 leaves its result
-// (lane (c, g): rows 4 g .. + 3 of column c), which is also the layout of its
-// second operand, and of its first for a symmetric matrix.  So A A, the polynomial
-// and X <- P X need no exchange; A = X X^T sums over columns, for which a block is
-// turned on its way through the wave's own piece of LDS (written in columns, read
-// with ds_read_b64_tr_b16), and the waves' sums are added through LDS.  One launch
-// instead of three a step: 64 matrices of [16, 2048] 124 us in tiles, 21 us here
-// (1024 of them 769 and 68; 64 of [32, 4096] 218 and 87).
+// Few rows (adapters): one workgroup takes a matrix through all steps. X stays in
+// registers (in the forms of 8 waves, past 2048 columns, which take all 256, 14 to
+// 32 of a lane's others go through scratch memory), in blocks of 16 x 16 as
+// v_mfma_f32_16x16x16_f16 leaves its result (lane (c, g): rows 4 g .. + 3 of column
+// c), which is also the layout of its second operand, and of its first for a
+// symmetric matrix. So A A, the polynomial and X <- P X need no exchange; A = X X^T
+// sums over columns, for which a block is turned on its way through the wave's own
+// piece of LDS (written in columns, read with ds_read_b64_tr_b16), and the waves'
+// sums are added through LDS. One launch instead of three a step: 64 matrices of
+// [16, 2048] 124 us in tiles, 21 us here (1024 of them 769 and 68; 64 of [32, 4096]
+// 218 and 87).
 // ---------------------------------------------------------------------------
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));

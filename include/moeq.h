@@ -552,10 +552,10 @@ moeq_status moeq_grouped_mm_fp8(const moeq_qweight *x, const moeq_qweight *w, co
  *   workspace of moeq_grouped_ffn_workspace_bytes(M, E, H, I), 16-byte aligned
  * g, u and the sums are fp32; h is rounded to bf16 for the down product.  The
  * same bits from run to run.  Rows of out and gu_saved outside [offsets[0],
- * offsets[E]) are not written, and such rows of x never reach a result.  Alignment, overlaps and offsets that do not
- * ascend as for moeq_grouped_mm.  MOEQ_ESHAPE unless moeq_grouped_mm and
- * moeq_grouped_mm_grad_input take both products (H and I multiples of 8, 4*I*H
- * < 2^31).  M == 0 is a valid no-op.
+ * offsets[E]) are not written, and such rows of x never reach a result.
+ * Alignment, overlaps and offsets that do not ascend as for moeq_grouped_mm.
+ * MOEQ_ESHAPE unless moeq_grouped_mm and moeq_grouped_mm_grad_input take both
+ * products (H and I multiples of 8, 4*I*H < 2^31).  M == 0 is a valid no-op.
  */
 size_t moeq_grouped_ffn_workspace_bytes(int32_t M, int32_t E, int32_t H, int32_t I);
 moeq_status moeq_grouped_ffn(const uint16_t *x_bf16, const uint16_t *gate_up_bf16, const uint16_t *down_bf16,
@@ -628,15 +628,14 @@ moeq_status moeq_clip_grad_norm(const moeq_grad *grads, int32_t count, double ma
  * coefficients may have any size (the polynomial's entries are kept to 2^-11 of
  * themselves, or to 2^-39 (|a| + |b| + |c|) where that is more), but have to keep
  * every singular value below 15.9 from step to step, or the result overflows.
- * Directions that
- * G lacks pick up fp16's rounding, which the steps raise with the small singular
- * values: with the usual coefficients and five steps, a [512, 1024] matrix of rank
- * one is 15 % off, of rank 4 7 %, 16 4.4 %, 64 2.2 %, 256 0.75 %, of full rank 0.2 %,
- * and other shapes alike.  The same bits from run to run.  An infinity or a NaN
- * makes its own matrix NaN.  MOEQ_EINVAL
- * for buffers that overlap, coefficients that are not finite and steps outside
- * 1..64; MOEQ_ESHAPE unless N and K are at most 2^20, the smaller at most 2^15,
- * E <= 65535 and E (N/256 + 1)(K/256 + 1) < 2^18.
+ * Directions that G lacks pick up fp16's rounding, which the steps raise with the
+ * small singular values: with the usual coefficients and five steps, a [512, 1024]
+ * matrix of rank one is 15 % off, of rank 4 7 %, 16 4.4 %, 64 2.2 %, 256 0.75 %, of
+ * full rank 0.2 %, and other shapes alike.  The same bits from run to run.  An
+ * infinity or a NaN makes its own matrix NaN.  MOEQ_EINVAL for buffers that
+ * overlap, coefficients that are not finite and steps outside 1..64; MOEQ_ESHAPE
+ * unless N and K are at most 2^20, the smaller at most 2^15, E <= 65535 and
+ * E (N/256 + 1)(K/256 + 1) < 2^18.
  */
 size_t moeq_orthogonalize_workspace_bytes(int32_t E, int32_t N, int32_t K);
 moeq_status moeq_orthogonalize(const void *g, int32_t dtype, int32_t E, int32_t N, int32_t K,
